@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "../../include/rsa.h"
+#include "../../include/rsa_rows.h"
 #include "../../include/rsa_sp.h"
 #include "rsa_internal.h"
 
@@ -279,7 +280,8 @@ rsa_status_t device_state(DeviceState **out) {
         if ((e = rsa::tc_kernels_configure()) != cudaSuccess ||
             (e = rsa::bwd_kernels_configure()) != cudaSuccess ||
             (e = rsa::fwd_kernels_configure()) != cudaSuccess ||
-            (e = rsa::linear_kernels_configure()) != cudaSuccess)
+            (e = rsa::linear_kernels_configure()) != cudaSuccess ||
+            (e = rsa::embed_kernels_configure()) != cudaSuccess)
             return cuda_fail("cudaFuncSetAttribute", e);
         void *ptr = nullptr;
         e = cudaGetSymbolAddress(&ptr, rsa::g_status_word);
@@ -304,12 +306,16 @@ rsa_status_t device_state(DeviceState **out) {
 
 enum Kind {
     K_QK_SLAB, K_SOFTMAX, K_PV, K_ROWDOT, K_BWD_KEYS, K_BWD_ROWS,
-    K_F32_QK, K_F32_PV, K_F32_BWD, K_F32_KEYS, K_F32_DQ, K_FWD_STATS, K_FWD_PV, K_SP_ACC, K_LINEAR, K_COUNT
+    K_F32_QK, K_F32_PV, K_F32_BWD, K_F32_KEYS, K_F32_DQ, K_FWD_STATS, K_FWD_PV, K_SP_ACC, K_LINEAR,
+    K_QK_NORM, K_QK_NORM_BWD, K_QK_DW, K_EMBED, K_EMBED_SORT, K_EMBED_GRAD, K_EMBED_JOIN,
+    K_DISTILL, K_DISTILL_BWD, K_DISTILL_STEP, K_COUNT
 };
 const char *kKindNames[K_COUNT] = {
     "qk_slab", "slab_softmax", "pv_softmax", "rowdot", "bwd_keys", "bwd_rows",
     "f32_qk_slab", "f32_pv_ring_rows", "f32_bwd_slab", "f32_ring_keys", "f32_dq_ring_rows",
-    "fwd_stats", "fwd_pv", "sp_accumulate", "linear"};
+    "fwd_stats", "fwd_pv", "sp_accumulate", "linear",
+    "qk_norm_rope", "qk_norm_rope_bwd", "qk_dw", "embed", "embed_sort", "embed_grad", "embed_join",
+    "distill", "distill_bwd", "distill_step"};
 
 struct ProfRec {
     int kind;
@@ -1020,6 +1026,366 @@ rsa_status_t rsa_linear(const void *X, const void *W, const float *bias, const v
     a.ntiles = (M / 128) * a.nNT;
     a.status = dev->status;
     RSA_LAUNCH(K_LINEAR, rsa::launch_linear(mX, mW, mY, a, dev->sms, s));
+    return RSA_OK;
+}
+
+// ---------------------------------------------------------------- row-local operators
+
+}  // extern "C"
+
+namespace {
+
+bool dtype_ok(rsa_dtype_t dt) { return dt == RSA_BF16 || dt == RSA_F32; }
+size_t dtype_bytes(rsa_dtype_t dt) { return dt == RSA_BF16 ? 2 : 4; }
+
+bool aligned_to(const void *p, size_t bytes) {
+    return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+
+// Whether the rows of d elements of a tensor with these strides and sizes keep clear of one
+// another: in the order of the strides, each step passes over all that lies below it.
+bool rows_apart(const long long *stride, const long long *size, int d) {
+    int order[3] = {0, 1, 2};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 3; ++j)
+            if (stride[order[j]] < stride[order[i]]) {
+                const int t = order[i];
+                order[i] = order[j], order[j] = t;
+            }
+    long long below = d;
+    for (int i = 0; i < 3; ++i) {
+        const int o = order[i];
+        if (size[o] <= 1) continue;
+        if (stride[o] < below) return false;
+        below = stride[o] * (size[o] - 1) + below;
+    }
+    return true;
+}
+
+// The checks the forward and the backward pass of the norm and rotation share; fills the
+// arguments that both have. `tensors` and `strides` go together, three strides per tensor
+// (shapes alternate between queries and keys); the last two tensors are written.
+rsa_status_t qk_args(rsa::QkArgs &a, const void *const *tensors, const long long *strides,
+                     int ntensors, const float *wq, const float *wk, const float *freq,
+                     const void *pos, int pos64, long long pos_sb, long long pos0, int B, int Hq,
+                     int Hk, int L, int d, int rot, int interleaved, float eps, rsa_dtype_t dt) {
+    if (B < 0 || L < 0 || Hq <= 0 || Hk <= 0 || !(eps > 0.f) || rot < 0 || rot > d || !strides)
+        return RSA_ERR_INVALID_ARG;
+    if (!dtype_ok(dt) || (d != 32 && d != 64 && d != 128) || rot % 16 != 0 ||
+        static_cast<long long>(B) * L > 0x7fffffffLL)
+        return RSA_ERR_UNSUPPORTED;
+    if (rot > 0 && (!freq || !aligned_to(freq, 4))) return RSA_ERR_INVALID_ARG;
+    if ((pos && !aligned_to(pos, pos64 ? 8 : 4)) || (wq && !aligned_to(wq, 4)) ||
+        (wk && !aligned_to(wk, 4)) || pos_sb < 0)
+        return RSA_ERR_INVALID_ARG;
+    const long long vec = 16 / static_cast<long long>(dtype_bytes(dt));
+    const bool rows = static_cast<long long>(B) * L > 0;  // without any, nothing is touched
+    for (int i = 0; rows && i < ntensors; ++i) {
+        if (!tensors[i] || !aligned16(tensors[i])) return RSA_ERR_INVALID_ARG;
+        const int H = i & 1 ? Hk : Hq;
+        const long long *s = strides + 3 * i;
+        const long long size[3] = {B, H, L};
+        for (int j = 0; j < 3; ++j) {
+            if (size[j] <= 1) continue;  // the stride of a single entry is not used
+            if (s[j] < 0 || s[j] % vec != 0) return RSA_ERR_INVALID_ARG;
+        }
+        if (i >= ntensors - 2 && !rows_apart(s, size, d)) return RSA_ERR_INVALID_ARG;
+        // an output in the place of an input has the input's layout, and is not another's
+        if (i >= ntensors - 2)
+            for (int k = 0; k < i; ++k) {
+                if (tensors[k] != tensors[i]) continue;
+                if ((k & 1) != (i & 1)) return RSA_ERR_INVALID_ARG;
+                for (int j = 0; j < 3; ++j)
+                    if (size[j] > 1 && strides[3 * k + j] != s[j]) return RSA_ERR_INVALID_ARG;
+            }
+    }
+    a.w[0] = wq, a.w[1] = wk;
+    a.H[0] = Hq, a.H[1] = Hk;
+    a.freq = freq;
+    a.pos = pos, a.pos64 = pos64 ? 1 : 0, a.pos_sb = pos_sb, a.pos0 = pos0;
+    a.B = B, a.L = L, a.d = d, a.rot = rot, a.inter = interleaved ? 1 : 0;
+    a.eps = eps;
+    return RSA_OK;
+}
+
+void copy_strides(long long (&to)[2][3], const long long *from) {
+    for (int i = 0; i < 6; ++i) to[i / 3][i % 3] = from[i];
+}
+
+// The embedding's sizes: 0 <= n < 2^31, 1 <= V < 2^31 - 1, 0 <= D <= 2^20, n D < 2^40.
+bool embed_sizes_ok(int n, int V, int D, rsa_status_t *why) {
+    if (n < 0 || V <= 0 || D < 0) {
+        *why = RSA_ERR_INVALID_ARG;
+        return false;
+    }
+    if (V == 0x7fffffff || D > (1 << 20) || static_cast<long long>(n) * D >= (1LL << 40)) {
+        *why = RSA_ERR_UNSUPPORTED;
+        return false;
+    }
+    return true;
+}
+
+// Whether rows of D elements of `bytes` each, `ld` apart, allow 16-byte accesses.
+bool rows_vec(const void *p, long long ld, int D, size_t bytes) {
+    return aligned16(p) && (ld * bytes) % 16 == 0 && (D * bytes) % 16 == 0;
+}
+
+struct EmbedLayout {
+    int S, npieces, Dp;
+    size_t list_bytes, key_bytes, part_bytes, total;
+};
+
+EmbedLayout embed_layout(int n, int D) {
+    EmbedLayout y{};
+    // pieces of 8 to 256 tokens, about 512 of them
+    const int s = (n / 512 + 7) / 8 * 8;
+    y.S = s < 8 ? 8 : s > 256 ? 256 : s;
+    y.npieces = n / y.S + (n % y.S != 0);
+    y.Dp = (D + 3) / 4 * 4;
+    y.key_bytes = align_up(size_t(n) * 4, kAlign);
+    y.list_bytes = align_up(size_t(y.npieces) * 4, kAlign);
+    y.part_bytes = size_t(y.npieces) * 2 * y.Dp * 4;
+    y.total = kAlign + y.list_bytes + 4 * y.key_bytes + align_up(y.part_bytes, kAlign);
+    return y;
+}
+
+// The checks the distillation's entry points share.
+rsa_status_t distill_args(rsa::DistillArgs &a, const void *logits, long long ld,
+                          const void *index, int index64, const void *teacher,
+                          rsa_dtype_t teacher_dt, int n, int V, int K, float temperature,
+                          rsa_dtype_t dt) {
+    if (n < 0 || V <= 0 || K <= 0 || !(temperature > 0.f) || isinf(temperature))
+        return RSA_ERR_INVALID_ARG;
+    if (!dtype_ok(dt) || !dtype_ok(teacher_dt) || K > RSA_DISTILL_MAX_K || V == 0x7fffffff ||
+        n >= (1 << 27))
+        return RSA_ERR_UNSUPPORTED;
+    if (n > 0 && (!logits || !index || !teacher || !aligned_to(logits, dtype_bytes(dt)) ||
+                  !aligned_to(index, index64 ? 8 : 4) ||
+                  !aligned_to(teacher, dtype_bytes(teacher_dt)) || (n > 1 && ld < 0)))
+        return RSA_ERR_INVALID_ARG;
+    a.z = logits, a.ld = ld;
+    a.index = index, a.index64 = index64 ? 1 : 0;
+    a.teacher = teacher, a.teacher_bf16 = teacher_dt == RSA_BF16;
+    a.n = n, a.V = V, a.K = K, a.tau = temperature;
+    return RSA_OK;
+}
+
+// The gradient's side of them: rows of dlogits apart, and equal to the logits' in place.
+bool distill_grad_ok(rsa::DistillArgs &a, const float *dloss, int dloss_stride, void *dlogits,
+                     long long ld_d, rsa_dtype_t dt) {
+    if (dloss_stride != 0 && dloss_stride != 1) return false;
+    if (a.n > 0 && (!dloss || !dlogits || !aligned_to(dloss, 4) ||
+                    !aligned_to(dlogits, dtype_bytes(dt)) || (a.n > 1 && ld_d < a.V) ||
+                    (dlogits == a.z && a.n > 1 && ld_d != a.ld)))
+        return false;
+    a.dloss = dloss, a.dloss_stride = dloss_stride;
+    a.dz = dlogits, a.ld_d = ld_d;
+    return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+rsa_status_t rsa_qk_norm_rope(const void *Q, const void *K, void *Qo, void *Ko,
+                              const long long *strides, const float *wq, const float *wk,
+                              const float *freq, const void *pos, int pos64,
+                              long long pos_batch_stride, long long pos0, int B, int Hq, int Hk,
+                              int L, int d, int rot, int interleaved, float eps, rsa_dtype_t dt,
+                              void *stream) {
+    rsa::QkArgs a{};
+    const void *tensors[] = {Q, K, Qo, Ko};
+    rsa_status_t st = qk_args(a, tensors, strides, 4, wq, wk, freq, pos, pos64, pos_batch_stride,
+                              pos0, B, Hq, Hk, L, d, rot, interleaved, eps, dt);
+    if (st != RSA_OK) return st;
+    if (static_cast<long long>(B) * L == 0) return RSA_OK;
+    a.x[0] = Q, a.x[1] = K, a.y[0] = Qo, a.y[1] = Ko;
+    copy_strides(a.sx, strides);
+    copy_strides(a.sy, strides + 6);
+    DeviceState *dev = nullptr;
+    st = device_state(&dev);
+    if (st != RSA_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    RSA_LAUNCH(K_QK_NORM, rsa::launch_qk_norm(a, 0, dt == RSA_BF16, dev->sms, s));
+    return RSA_OK;
+}
+
+size_t rsa_qk_norm_rope_workspace_size(int d) {
+    if (d != 32 && d != 64 && d != 128) return 0;
+    return size_t(rsa::kQkBlocksPerSm) * rsa::kQkMaxSms * d * 4;
+}
+
+rsa_status_t rsa_qk_norm_rope_backward(const void *Q, const void *K, const void *dQo,
+                                       const void *dKo, void *dQ, void *dK,
+                                       const long long *strides, const float *wq, const float *wk,
+                                       float *dwq, float *dwk, const float *freq, const void *pos,
+                                       int pos64, long long pos_batch_stride, long long pos0,
+                                       int B, int Hq, int Hk, int L, int d, int rot,
+                                       int interleaved, float eps, rsa_dtype_t dt,
+                                       void *workspace, size_t ws_bytes, void *stream) {
+    rsa::QkArgs a{};
+    const void *tensors[] = {Q, K, dQo, dKo, dQ, dK};
+    rsa_status_t st = qk_args(a, tensors, strides, 6, wq, wk, freq, pos, pos64, pos_batch_stride,
+                              pos0, B, Hq, Hk, L, d, rot, interleaved, eps, dt);
+    if (st != RSA_OK) return st;
+    if ((dwq && !aligned_to(dwq, 4)) || (dwk && !aligned_to(dwk, 4))) return RSA_ERR_INVALID_ARG;
+    a.dw[0] = dwq, a.dw[1] = dwk;
+    const bool rows = static_cast<long long>(B) * L > 0;
+    const bool weights = dwq || dwk;
+    if (!rows && !weights) return RSA_OK;
+    if (rows && weights) {
+        if (ws_bytes < rsa_qk_norm_rope_workspace_size(d)) return RSA_ERR_WORKSPACE;
+        if (!ws_ok(workspace)) return RSA_ERR_INVALID_ARG;
+        a.part = static_cast<float *>(workspace);
+    }
+    a.x[0] = Q, a.x[1] = K, a.dy[0] = dQo, a.dy[1] = dKo, a.y[0] = dQ, a.y[1] = dK;
+    copy_strides(a.sx, strides);
+    copy_strides(a.sdy, strides + 6);
+    copy_strides(a.sy, strides + 12);
+    DeviceState *dev = nullptr;
+    st = device_state(&dev);
+    if (st != RSA_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (rows) RSA_LAUNCH(K_QK_NORM_BWD, rsa::launch_qk_norm(a, 1, dt == RSA_BF16, dev->sms, s));
+    if (weights) RSA_LAUNCH(K_QK_DW, rsa::launch_qk_dw(a, s));  // no rows: zeros
+    return RSA_OK;
+}
+
+rsa_status_t rsa_embed(const void *ids, int ids64, const void *table, long long ld_table,
+                       void *out, long long ld_out, int n, int V, int D, float scale,
+                       rsa_dtype_t dt, void *stream) {
+    rsa_status_t why;
+    if (!embed_sizes_ok(n, V, D, &why)) return why;
+    if (!dtype_ok(dt)) return RSA_ERR_UNSUPPORTED;
+    if (n == 0 || D == 0) return RSA_OK;
+    const size_t e = dtype_bytes(dt);
+    if (!ids || !table || !out || !aligned_to(ids, ids64 ? 8 : 4) || !aligned_to(table, e) ||
+        !aligned_to(out, e) || (V > 1 && ld_table < D) || (n > 1 && ld_out < D) || table == out)
+        return RSA_ERR_INVALID_ARG;
+    DeviceState *dev = nullptr;
+    const rsa_status_t st = device_state(&dev);
+    if (st != RSA_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    rsa::EmbedArgs a{};
+    a.ids = ids, a.ids64 = ids64 ? 1 : 0, a.n = n, a.V = V, a.D = D, a.scale = scale;
+    a.table = table, a.out = out, a.ld_table = ld_table, a.ld_out = ld_out;
+    const int vec = rows_vec(table, ld_table, D, e) && rows_vec(out, ld_out, D, e);
+    RSA_LAUNCH(K_EMBED, rsa::launch_embed(a, dt == RSA_BF16, vec, s));
+    return RSA_OK;
+}
+
+size_t rsa_embed_workspace_size(int n, int V, int D) {
+    rsa_status_t why;
+    if (!embed_sizes_ok(n, V, D, &why) || n == 0 || D == 0) return 0;
+    return embed_layout(n, D).total;
+}
+
+rsa_status_t rsa_embed_backward(const void *ids, int ids64, const void *dout, long long ld_dout,
+                                void *dtable, long long ld_dtable, int n, int V, int D,
+                                float scale, int accumulate, rsa_dtype_t dt, rsa_dtype_t dt_table,
+                                void *workspace, size_t ws_bytes, void *stream) {
+    rsa_status_t why;
+    if (!embed_sizes_ok(n, V, D, &why)) return why;
+    if (!dtype_ok(dt) || (dt_table != dt && dt_table != RSA_F32)) return RSA_ERR_UNSUPPORTED;
+    if (D == 0 || (n == 0 && accumulate)) return RSA_OK;
+    const size_t e = dtype_bytes(dt), et = dtype_bytes(dt_table);
+    if (!dtable || !aligned_to(dtable, et) || (V > 1 && ld_dtable < D)) return RSA_ERR_INVALID_ARG;
+    if (n > 0) {
+        if (!ids || !dout || !aligned_to(ids, ids64 ? 8 : 4) || !aligned_to(dout, e) ||
+            (n > 1 && ld_dout < 0) || dout == dtable)
+            return RSA_ERR_INVALID_ARG;
+        if (ws_bytes < embed_layout(n, D).total) return RSA_ERR_WORKSPACE;
+        if (!ws_ok(workspace)) return RSA_ERR_INVALID_ARG;
+    }
+    DeviceState *dev = nullptr;
+    const rsa_status_t st = device_state(&dev);
+    if (st != RSA_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (n == 0) {  // no token: zeros
+        RSA_TRY(cudaMemset2DAsync(dtable, (V > 1 ? ld_dtable : D) * et, 0, D * et, V, s));
+        return RSA_OK;
+    }
+    const EmbedLayout y = embed_layout(n, D);
+    rsa::EmbedArgs a{};
+    a.ids = ids, a.ids64 = ids64 ? 1 : 0, a.n = n, a.V = V, a.D = D, a.scale = scale;
+    a.dout = dout, a.dtable = dtable, a.ld_dout = ld_dout, a.ld_dtable = ld_dtable;
+    a.accumulate = accumulate ? 1 : 0;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    a.count = reinterpret_cast<uint32_t *>(ws);
+    a.list = reinterpret_cast<uint32_t *>(ws += kAlign);
+    ws += y.list_bytes;
+    for (int i = 0; i < 2; ++i) {
+        a.key[i] = reinterpret_cast<uint32_t *>(ws);
+        a.idx[i] = reinterpret_cast<uint32_t *>(ws + y.key_bytes);
+        ws += 2 * y.key_bytes;
+    }
+    a.part = reinterpret_cast<float *>(ws);
+    a.S = y.S, a.npieces = y.npieces, a.Dp = y.Dp;
+    rsa::embed_sort_plan(a);
+    const int out16 = dt_table == RSA_BF16;
+    const int vec = rows_vec(dout, ld_dout, D, e) && rows_vec(dtable, ld_dtable, D, et);
+    RSA_LAUNCH(K_EMBED_SORT, rsa::launch_embed_sort(a, out16, vec, dev->sms, s));
+    RSA_LAUNCH(K_EMBED_GRAD, rsa::launch_embed_grad(a, dt == RSA_BF16, out16, vec, s));
+    RSA_LAUNCH(K_EMBED_JOIN, rsa::launch_embed_join(a, out16, dev->sms, s));
+    return RSA_OK;
+}
+
+rsa_status_t rsa_distill(const void *logits, long long ld, const void *index, int index64,
+                         const void *teacher, rsa_dtype_t teacher_dt, float *loss, float *stats,
+                         int n, int V, int K, float temperature, rsa_dtype_t dt, void *stream) {
+    rsa::DistillArgs a{};
+    rsa_status_t st = distill_args(a, logits, ld, index, index64, teacher, teacher_dt, n, V, K,
+                                   temperature, dt);
+    if (st != RSA_OK) return st;
+    if (n == 0) return RSA_OK;
+    if (!loss || !stats || !aligned_to(loss, 4) || !aligned_to(stats, 8)) return RSA_ERR_INVALID_ARG;
+    a.loss = loss, a.stats = reinterpret_cast<float2 *>(stats);
+    DeviceState *dev = nullptr;
+    st = device_state(&dev);
+    if (st != RSA_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    RSA_LAUNCH(K_DISTILL, rsa::launch_distill(a, 0, dt == RSA_BF16, dev->sms, s));
+    return RSA_OK;
+}
+
+rsa_status_t rsa_distill_backward(const void *logits, long long ld, const void *index, int index64,
+                                  const void *teacher, rsa_dtype_t teacher_dt, const float *stats,
+                                  const float *dloss, int dloss_stride, void *dlogits,
+                                  long long ld_d, int n, int V, int K, float temperature,
+                                  rsa_dtype_t dt, void *stream) {
+    rsa::DistillArgs a{};
+    rsa_status_t st = distill_args(a, logits, ld, index, index64, teacher, teacher_dt, n, V, K,
+                                   temperature, dt);
+    if (st != RSA_OK) return st;
+    if (!distill_grad_ok(a, dloss, dloss_stride, dlogits, ld_d, dt)) return RSA_ERR_INVALID_ARG;
+    if (n == 0) return RSA_OK;
+    if (!stats || !aligned_to(stats, 8)) return RSA_ERR_INVALID_ARG;
+    a.stats = reinterpret_cast<float2 *>(const_cast<float *>(stats));
+    DeviceState *dev = nullptr;
+    st = device_state(&dev);
+    if (st != RSA_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    RSA_LAUNCH(K_DISTILL_BWD, rsa::launch_distill(a, 1, dt == RSA_BF16, dev->sms, s));
+    return RSA_OK;
+}
+
+rsa_status_t rsa_distill_step(const void *logits, long long ld, const void *index, int index64,
+                              const void *teacher, rsa_dtype_t teacher_dt, const float *dloss,
+                              int dloss_stride, float *loss, void *dlogits, long long ld_d, int n,
+                              int V, int K, float temperature, rsa_dtype_t dt, void *stream) {
+    rsa::DistillArgs a{};
+    rsa_status_t st = distill_args(a, logits, ld, index, index64, teacher, teacher_dt, n, V, K,
+                                   temperature, dt);
+    if (st != RSA_OK) return st;
+    if (!distill_grad_ok(a, dloss, dloss_stride, dlogits, ld_d, dt)) return RSA_ERR_INVALID_ARG;
+    if (n == 0) return RSA_OK;
+    if (!loss || !aligned_to(loss, 4)) return RSA_ERR_INVALID_ARG;
+    a.loss = loss;
+    DeviceState *dev = nullptr;
+    st = device_state(&dev);
+    if (st != RSA_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    RSA_LAUNCH(K_DISTILL_STEP, rsa::launch_distill(a, 2, dt == RSA_BF16, dev->sms, s));
     return RSA_OK;
 }
 

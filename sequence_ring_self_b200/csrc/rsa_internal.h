@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "../../include/rsa.h"
+#include "../../include/rsa_rows.h"
 
 namespace rsa {
 
@@ -126,6 +127,72 @@ struct LinArgs {
 cudaError_t launch_linear(const CUtensorMap &mX, const CUtensorMap &mW, const CUtensorMap &mY,
                           const LinArgs &a, int num_sms, cudaStream_t st);
 cudaError_t linear_kernels_configure();
+
+// ---- row-local operators (kernels_qknorm.cu, kernels_embed.cu, kernels_distill.cu) ------------
+// Norm and rotation of queries (side 0) and keys (side 1). Strides: (batch, head, row).
+constexpr int kQkBlocksPerSm = 4, kQkMaxSms = 160;  // the backward kernel's blocks, at most
+struct QkArgs {
+    const void *x[2], *dy[2];  // inputs; the outputs' gradients (backward)
+    void *y[2];                // outputs; backward: the inputs' gradients
+    long long sx[2][3], sdy[2][3], sy[2][3];
+    const float *w[2];         // [d] or null
+    float *dw[2];              // backward: [d] or null
+    float *part;               // backward: [blocks][d], null when no dw is wanted
+    int H[2];
+    const float *freq;
+    const void *pos;
+    long long pos_sb, pos0;
+    int pos64, B, L, d, rot, inter;
+    float eps;
+    int logP;     // rows per tile, set by the launch
+    int nblk[2];  // backward: blocks of each side, set by the launch
+};
+cudaError_t launch_qk_norm(QkArgs &a, int backward, int bf16, int num_sms, cudaStream_t st);
+// The weights' gradients from a.part, after the backward launch that set a.nblk.
+cudaError_t launch_qk_dw(const QkArgs &a, cudaStream_t st);
+
+struct EmbedArgs {
+    const void *ids;
+    int ids64, n, V, D;
+    float scale;
+    const void *table;  // lookup
+    void *out;
+    long long ld_table, ld_out;
+    const void *dout;   // gradient
+    void *dtable;
+    long long ld_dout, ld_dtable;
+    int accumulate;
+    int passes, bits;                // the sort's passes and the bits of a digit
+    uint32_t *key[2], *idx[2];       // the sorted ids and their tokens: [0] in the end
+    uint32_t *count, *list;          // pieces whose last id goes on behind them
+    float *part;                     // [npieces][2][Dp] partial rows
+    int S, npieces, Dp;
+};
+// vec: rows and columns allow 16-byte accesses.
+cudaError_t launch_embed(const EmbedArgs &a, int bf16, int vec, cudaStream_t st);
+void embed_sort_plan(EmbedArgs &a);  // sets a.passes and a.bits for a.V
+// Sort, sums, joins; bf16_out: the table's gradient is bf16 (fp32 otherwise).
+cudaError_t launch_embed_sort(const EmbedArgs &a, int bf16_out, int vec, int num_sms,
+                              cudaStream_t st);
+cudaError_t launch_embed_grad(const EmbedArgs &a, int bf16, int bf16_out, int vec, cudaStream_t st);
+cudaError_t launch_embed_join(const EmbedArgs &a, int bf16_out, int num_sms, cudaStream_t st);
+cudaError_t embed_kernels_configure();
+
+struct DistillArgs {
+    const void *z, *index, *teacher;
+    long long ld, ld_d;
+    int index64, teacher_bf16;
+    float *loss;
+    float2 *stats;
+    const float *dloss;
+    int dloss_stride;
+    void *dz;
+    int n, V, K;
+    float tau;
+    int cluster;  // CTAs per row, set by the launch
+};
+// mode: 0 loss and statistics, 1 gradient, 2 loss and gradient.
+cudaError_t launch_distill(DistillArgs a, int mode, int bf16, int num_sms, cudaStream_t st);
 
 // ---- CUDA-core kernels (kernels_simt.cu) -----------------------------------------------
 // Row softmax of the group's fp32 slab, in place: P written as bf16 (p_bf16 = 1) into the

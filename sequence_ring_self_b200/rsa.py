@@ -32,7 +32,11 @@ EXPORTED = ("rsa_workspace_size", "rsa_forward", "rsa_backward", "rsa_status_str
             "rsa_debug_report_status",
             # include/rsa_sp.h
             "rsa_sp_workspace_size", "rsa_sp_scores", "rsa_sp_softmax_pv", "rsa_sp_backward_rows",
-            "rsa_sp_backward_keys", "rsa_sp_accumulate", "rsa_linear")
+            "rsa_sp_backward_keys", "rsa_sp_accumulate", "rsa_linear",
+            # include/rsa_rows.h
+            "rsa_qk_norm_rope", "rsa_qk_norm_rope_workspace_size", "rsa_qk_norm_rope_backward",
+            "rsa_embed", "rsa_embed_workspace_size", "rsa_embed_backward", "rsa_distill",
+            "rsa_distill_backward", "rsa_distill_step")
 
 _lib = None
 _lock = threading.Lock()
@@ -99,6 +103,25 @@ def load_library(path: str | None = None):
         lib.rsa_debug_report_status.restype = i
         lib.rsa_linear.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, vp]
         lib.rsa_linear.restype = i
+        f, ll, st = ctypes.c_float, ctypes.c_longlong, ctypes.POINTER(ctypes.c_longlong)
+        qk = [vp, i, ll, ll, i, i, i, i, i, i, i, f, i]  # positions .. dtype
+        lib.rsa_qk_norm_rope.argtypes = [vp, vp, vp, vp, st, vp, vp, vp, *qk, vp]
+        lib.rsa_qk_norm_rope_workspace_size.argtypes = [i]
+        lib.rsa_qk_norm_rope_workspace_size.restype = sz
+        lib.rsa_qk_norm_rope_backward.argtypes = [vp, vp, vp, vp, vp, vp, st, vp, vp, vp, vp, vp,
+                                                  *qk, vp, sz, vp]
+        lib.rsa_embed.argtypes = [vp, i, vp, ll, vp, ll, i, i, i, f, i, vp]
+        lib.rsa_embed_workspace_size.argtypes = [i, i, i]
+        lib.rsa_embed_workspace_size.restype = sz
+        lib.rsa_embed_backward.argtypes = [vp, i, vp, ll, vp, ll, i, i, i, f, i, i, i, vp, sz, vp]
+        lib.rsa_distill.argtypes = [vp, ll, vp, i, vp, i, vp, vp, i, i, i, f, i, vp]
+        lib.rsa_distill_backward.argtypes = [vp, ll, vp, i, vp, i, vp, vp, i, vp, ll, i, i, i, f, i,
+                                             vp]
+        lib.rsa_distill_step.argtypes = [vp, ll, vp, i, vp, i, vp, i, vp, vp, ll, i, i, i, f, i, vp]
+        for name in ("rsa_qk_norm_rope", "rsa_qk_norm_rope_backward", "rsa_embed",
+                     "rsa_embed_backward", "rsa_distill", "rsa_distill_backward",
+                     "rsa_distill_step"):
+            getattr(lib, name).restype = i
         if path is None:
             _lib = lib
         return lib
