@@ -2,13 +2,11 @@
 // position, in one pass, forward and backward (rsa_qk_norm_rope, rsa_rows.h).
 //
 // Bound by memory: a forward pass reads and writes every element once (2 x 2 bytes in bf16)
-// and spends about ten operations on it. A row of d elements lies in the 16-byte vectors of
-// d / 8 (bf16) or d / 4 (fp32) neighbouring lanes, so a row's sum is a few shuffles, and the
-// other member of a half-split pair is one shuffle of the packed vector away. A tile is P
-// consecutive rows of the sequence for all heads of one side (queries or keys): the tile's
-// P x rot/2 angles are computed once by the block (fp64 product and reduction, fp32 sine and
-// cosine) and every thread keeps the position and columns it serves, so the head loop has the
-// cosines, sines and weights in registers and only streams rows.
+// and spends about ten operations on it, a backward pass three times and twenty. Rows are held
+// in 16-byte vectors by neighbouring lanes, so that a row's sums are a few shuffles. A tile is P
+// consecutive rows of the sequence for all heads of one side (queries or keys): the tile's angles
+// are computed once by the block (fp64 product and reduction, fp32 sine and cosine) and a thread
+// keeps the row and columns it serves, so the head loop only streams rows.
 #include <type_traits>
 
 #include "rows_common.cuh"
@@ -25,63 +23,89 @@ __device__ __forceinline__ long long position(const QkArgs &a, unsigned b, unsig
     return index_at(a.pos, a.pos64, static_cast<long long>(b) * a.pos_sb + l);
 }
 
-// (cos, sin) of position * freq. The angle in turns is formed and reduced in fp64: the product
-// of a position below 2^29 with an fp32 frequency is exact, and the reduced turn carries an
-// error near 2^-53 of the whole angle.
-__device__ __forceinline__ float2 angle(long long pos, float freq) {
-    const double turns = static_cast<double>(pos) * static_cast<double>(freq) * 0.15915494309189533577;
+__device__ __forceinline__ double turns_per_unit(long long pos) {
+    return static_cast<double>(pos) * 0.15915494309189533577;  // 1 / 2 pi
+}
+
+// (cos, sin) of position * freq, pos = position / 2 pi. The angle in turns is formed and reduced
+// in fp64: its error is about 2^-52 of the whole angle.
+__device__ __forceinline__ float2 angle(double pos, float freq) {
+    const double turns = pos * static_cast<double>(freq);
     float2 cs;
     sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &cs.y, &cs.x);
     return cs;
 }
 
-// A thread's part of the rotation for its VEC columns: y_e = n_e c_e + n_partner(e) s_e, with
-// s_e = -sin for the first and +sin for the second member of a pair (columns past rot: 1, 0).
+// Backward: a row of D = 2 LPR VEC elements is held by LPR lanes, two vectors each: the pairs' first and
+// second members where half-split pairs are rotated (the first rot / 2 / VEC lanes; the others
+// share the vectors behind rot), halves of the row with neighbouring pairs.
 template <int LPR, int VEC, bool INTER>
-struct Rotation {
-    float c[VEC], s[VEC];
+__device__ __forceinline__ void lane_columns(int t, int rot, int (&col)[2]) {
+    const int nl = INTER ? 0 : rot / 2 / VEC;
+    if (t < nl)
+        col[0] = t, col[1] = t + nl;
+    else
+        col[0] = t + nl, col[1] = t + LPR;
+    col[0] *= VEC, col[1] *= VEC;
+}
 
-    __device__ __forceinline__ static int partner_lane(int li, int rot) {
-        const int nl = rot / 2 / VEC;  // lanes of the half-split pairs' first members
-        return INTER || li >= 2 * nl ? li : (li < nl ? li + nl : li - nl);
+// Rotation factors, VEC pairs per lane: pair j of the row lies at factor_at(j) of each of the
+// tile row's three lists of D / 2 numbers: cos, sin, -sin. Pairs behind rot / 2 have (1, 0, 0).
+// Neighbouring lanes' four-number accesses are neighbours: a warp's read has no bank conflict.
+template <int LPR, int VEC, bool INTER>
+__device__ __forceinline__ int factor_at(int j) {
+    int t = j / VEC, e = j % VEC;
+    if (INTER) {  // VEC / 2 pairs of each of the lane's vectors
+        const int v = j / (VEC / 2);
+        t = v % LPR, e = j % (VEC / 2) + v / LPR * (VEC / 2);
     }
-    __device__ __forceinline__ void load(const float2 *cs, int li, int rot) {
-        const int col = li * VEC, half = rot / 2;
-        if (INTER) {
-#pragma unroll
-            for (int e = 0; e < VEC; e += 2) {
-                const float2 t = col < rot ? cs[col / 2 + e / 2] : make_float2(1.f, 0.f);
-                c[e] = c[e + 1] = t.x;
-                s[e] = -t.y, s[e + 1] = t.y;
-            }
-        } else {
-            const bool second = col >= half;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float2 t =
-                    col < rot ? cs[col + e - (second ? half : 0)] : make_float2(1.f, 0.f);
-                c[e] = t.x;
-                s[e] = second ? t.y : -t.y;
-            }
-        }
-    }
-};
+    return e / 4 * (LPR * 4) + t * 4 + e % 4;
+}
 
-// The vector of the pair partners: the neighbouring elements, or the partner lane's vector.
-template <int VEC, bool INTER, typename P>
-__device__ __forceinline__ void partners(const P &v, const float (&f)[VEC], int lane, float (&g)[VEC]) {
-    if constexpr (INTER) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) g[e] = f[e ^ 1];
-    } else {
-        P w;
-        w.raw.x = __shfl_sync(0xffffffffu, v.raw.x, lane);
-        w.raw.y = __shfl_sync(0xffffffffu, v.raw.y, lane);
-        w.raw.z = __shfl_sync(0xffffffffu, v.raw.z, lane);
-        w.raw.w = __shfl_sync(0xffffffffu, v.raw.w, lane);
-        w.to(g);
+// The block fills cs[p][3][D / 2] for the tile's rows p < P, each row by 256 / P threads.
+template <int LPR, int VEC, bool INTER>
+__device__ __forceinline__ void tile_factors(const QkArgs &a, unsigned m0, unsigned M, float *cs) {
+    constexpr int N = LPR * VEC;  // pairs of a row
+    const int per = kThreads >> a.logP, p = threadIdx.x / per, half = a.rot / 2;
+    const unsigned m = m0 + p;
+    if (m >= M) return;
+    const unsigned b = m / a.L;
+    const double pos = turns_per_unit(position(a, b, m - b * a.L));
+    float *row = cs + p * 3 * N;
+    for (int j = threadIdx.x & (per - 1); j < N; j += per) {
+        const float2 t = j < half ? angle(pos, a.freq[j]) : make_float2(1.f, 0.f);
+        const int at = factor_at<LPR, VEC, INTER>(j);
+        row[at] = t.x;
+        row[N + at] = t.y;
+        row[2 * N + at] = -t.y;
     }
 }
+
+// The same for one number per column, VEC columns per lane.
+template <int LPR, int VEC>
+__device__ __forceinline__ int column_at(int col) {
+    return col % VEC / 4 * (LPR * 4) + col / VEC * 4 + col % 4;
+}
+
+// A lane's VEC numbers of one list.
+template <int LPR, int VEC>
+__device__ __forceinline__ void load_factors(const float *list, int t, float2 (&f)[VEC / 2]) {
+#pragma unroll
+    for (int e = 0; e < VEC; e += 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(list + e * LPR + t * 4);
+        f[e / 2] = make_float2(v.x, v.y);
+        f[e / 2 + 1] = make_float2(v.z, v.w);
+    }
+}
+
+// With neighbouring pairs, pair i of vector k of the lane: its number of a list of VEC.
+template <int VEC>
+__device__ __forceinline__ float of_pair(const float2 (&f)[VEC / 2], int k, int i) {
+    const int n = k * (VEC / 2) + i;
+    return n & 1 ? f[n / 2].y : f[n / 2].x;
+}
+
+__device__ __forceinline__ float2 swapped(float2 v) { return make_float2(v.y, v.x); }
 
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x) {
@@ -90,184 +114,289 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
-// The tile's angles: cs[p][i], p < P rows, i < rot / 2.
-__device__ __forceinline__ void tile_angles(const QkArgs &a, unsigned m0, unsigned M, float2 *cs) {
-    const int half = a.rot / 2, n = half << a.logP;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const int p = i / half, j = i - p * half;
-        const unsigned m = m0 + p;
-        if (m < M) {
-            const unsigned b = m / a.L;
-            cs[i] = angle(position(a, b, m - b * a.L), a.freq[j]);
-        }
-    }
+// VEC weights from a column on, in pairs, by way of shared memory (the caller's array need not
+// be aligned for vector loads).
+template <int VEC>
+__device__ __forceinline__ void load_weights(const float *sw, int col, float2 (&w)[VEC / 2]) {
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) w[e] = reinterpret_cast<const float2 *>(sw + col)[e];
 }
 
-// Forward: grid (tiles of P rows, side). Four rows per thread are in flight.
+// Forward: grid (tiles of P rows, side); one vector of a row per lane, LPR lanes per row, four rows
+// per thread in flight. With the weights folded in, a column has two factors,
+//   y_e = r (x_e f_e + x_partner(e) g_e),
+// which the block leaves in shared memory for the tile's rows and a thread keeps for its own.
+// The partner's vector comes by shuffles of the packed one: against two vectors per thread
+// (as in the backward pass) this has more instructions, but whole 128-byte rows per access at
+// d = 64 and more blocks per SM: 28.1 us against 37.2 for 4 x 4096 rows of 16 + 16 heads of 64.
 template <typename T, int LPR, bool INTER>
 __global__ void __launch_bounds__(kThreads) qk_norm_kernel(const QkArgs a) {
-    constexpr int VEC = 16 / sizeof(T), D = LPR * VEC, R = kThreads / LPR, U = 4;
+    constexpr int VEC = 16 / sizeof(T), D = LPR * VEC, R = kThreads / LPR, U = 4, E = VEC / 2;
     using P = Pack<T, VEC>;
-    __shared__ float2 cs[R * D / 2];
+    __shared__ __align__(16) float cs[R * 2 * D];  // [p][f, g][D]
     pdl_wait();
     const int side = blockIdx.y, H = a.H[side];
-    const int li = threadIdx.x % LPR, g = threadIdx.x / LPR;
+    const int t = threadIdx.x % LPR, g = threadIdx.x / LPR;
     const int p = g & ((1 << a.logP) - 1), h0 = g >> a.logP, HG = R >> a.logP;
     const unsigned M = static_cast<unsigned>(a.B) * a.L, m0 = blockIdx.x << a.logP, m = m0 + p;
     const bool live = m < M;
     const unsigned b = live ? m / a.L : 0, l = live ? m - b * a.L : 0;
-    const T *x = static_cast<const T *>(a.x[side]) + b * a.sx[side][0] + l * a.sx[side][2] + li * VEC;
-    T *y = static_cast<T *>(a.y[side]) + b * a.sy[side][0] + l * a.sy[side][2] + li * VEC;
-    const long long hx = a.sx[side][1], hy = a.sy[side][1];
+    const long long hx = a.sx[side][1] * HG, hy = a.sy[side][1] * HG;  // to the next round's head
+    const T *x = static_cast<const T *>(a.x[side]) + b * a.sx[side][0] + l * a.sx[side][2] +
+                 a.sx[side][1] * h0 + t * VEC;
+    T *y = static_cast<T *>(a.y[side]) + b * a.sy[side][0] + l * a.sy[side][2] +
+           a.sy[side][1] * h0 + t * VEC;
+    const int left = live && h0 < H ? (H - h0 + HG - 1) / HG : 0;  // this thread's rows
 
     P v[U];  // the first rows travel while the angles are computed
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * HG;
-        v[u] = live && h < H ? P::load(x + h * hx) : P::zero();
-    }
-    tile_angles(a, m0, M, cs);
-    __syncthreads();
-    // y_e = r (x_e w_e c_e + x_partner w_partner s_e): weights folded into the rotation
-    Rotation<LPR, VEC, INTER> rt;
-    rt.load(cs + p * (a.rot / 2), li, a.rot);
-    const int pl = Rotation<LPR, VEC, INTER>::partner_lane(li, a.rot);
-    if (const float *w = a.w[side]) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            rt.c[e] *= w[li * VEC + e];
-            rt.s[e] *= w[INTER ? li * VEC + (e ^ 1) : pl * VEC + e];
+    for (int u = 0; u < U; ++u, x += hx) v[u] = u < left ? P::load(x) : P::zero();
+    {
+        const int per = kThreads >> a.logP, q = threadIdx.x / per, half = a.rot / 2;
+        const unsigned mq = m0 + q;
+        if (mq < M) {
+            const unsigned bq = mq / a.L;
+            const double pos = turns_per_unit(position(a, bq, mq - bq * a.L));
+            const float *w = a.w[side];
+            float *row = cs + q * 2 * D;
+            for (int j = threadIdx.x & (per - 1); j < D / 2; j += per) {
+                const float2 cj = j < half ? angle(pos, a.freq[j]) : make_float2(1.f, 0.f);
+                // the pair's columns; behind rot two that are left as they are
+                const int c0 = INTER || j >= half ? 2 * j : j, c1 = INTER || j >= half ? c0 + 1 : j + half;
+                const float w0 = w ? w[c0] : 1.f, w1 = w ? w[c1] : 1.f;
+                const int u = column_at<LPR, VEC>(c0), z = column_at<LPR, VEC>(c1);
+                row[u] = cj.x * w0, row[z] = cj.x * w1;
+                row[D + u] = -cj.y * w1, row[D + z] = cj.y * w0;
+            }
         }
     }
-    const int src = (threadIdx.x & 31 & ~(LPR - 1)) | pl;
-    for (int h = h0; h - h0 < H; h += U * HG) {  // the same count for every thread
+    __syncthreads();
+    float2 f0[E], f1[E];
+    load_factors<LPR, VEC>(cs + p * 2 * D, t, f0);
+    load_factors<LPR, VEC>(cs + p * 2 * D + D, t, f1);
+    const int nl = a.rot / 2 / VEC;  // lanes of the half-split pairs' first members
+    const int partner = t < nl ? t + nl : t < 2 * nl ? t - nl : t;
+    const int src = (threadIdx.x & 31 & ~(LPR - 1)) | partner;
+    for (int i = 0; i * HG < H; i += U) {  // the same count for every thread
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float f[VEC], q[VEC], ss = 0.f;
+            float2 f[E], q[E], ss = make_float2(0.f, 0.f);
             v[u].to(f);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) ss = fmaf(f[e], f[e], ss);
-            const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps);
-            partners<VEC, INTER>(v[u], f, src, q);
+            for (int e = 0; e < E; ++e) ss = fma2(f[e], f[e], ss);
+            const float2 r = both(rsqrtf(row_sum<LPR>(ss.x + ss.y) * (1.f / D) + a.eps));
+            if (INTER) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) f[e] = r * fmaf(f[e], rt.c[e], q[e] * rt.s[e]);
-            const int hu = h + u * HG, hn = hu + U * HG;
-            if (live && hu < H) P::from(f).store(y + hu * hy);
-            if (live && hn < H) v[u] = P::load(x + hn * hx);
+                for (int e = 0; e < E; ++e) q[e] = swapped(f[e]);
+            } else {
+                P w;
+                w.raw.x = __shfl_sync(0xffffffffu, v[u].raw.x, src);
+                w.raw.y = __shfl_sync(0xffffffffu, v[u].raw.y, src);
+                w.raw.z = __shfl_sync(0xffffffffu, v[u].raw.z, src);
+                w.raw.w = __shfl_sync(0xffffffffu, v[u].raw.w, src);
+                w.to(q);
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) f[e] = mul2(r, fma2(f[e], f0[e], mul2(q[e], f1[e])));
+            if (i + u < left) P::from(f).store(y);
+            if (i + u + U < left) v[u] = P::load(x);
+            x += hx;
+            y += hy;
         }
     }
 }
 
 // Backward: persistent blocks, the first nblk[0] on the queries and the rest on the keys, each
 // over the tiles of its side; a thread's columns are the same in all of them, so the weights'
-// gradient is summed in registers and the block leaves one row of sums in `part`.
+// gradient is summed in registers and the block leaves one row of sums in `part`. Rows travel
+// through kStages slots of each thread by asynchronous copies, two rows ahead and across
+// tiles; the factors of the next tile are computed while this one's rows arrive. Both members of
+// a pair are the thread's own: with one vector per thread and the partner's fetched by shuffles
+// the kernel was bound by its instructions (86 us instead of 70 for 16384 rows of 16 + 16 heads of
+// 128, bf16: 402 MB, 88% of a copy's rate).
+constexpr int kStages = 3;
+
 template <typename T, int LPR, bool INTER>
-__global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(const QkArgs a) {
-    constexpr int VEC = 16 / sizeof(T), D = LPR * VEC, R = kThreads / LPR, U = 2;
+__global__ void __launch_bounds__(kThreads, kQkBlocksPerSm) qk_norm_bwd_kernel(const QkArgs a) {
+    constexpr int VEC = 16 / sizeof(T), N = LPR * VEC, D = 2 * N, R = kThreads / LPR, E = VEC / 2;
     using P = Pack<T, VEC>;
-    __shared__ float2 cs[R * D / 2];  // the sums' exchange at the end: R x D floats
+    extern __shared__ __align__(16) uint8_t dyn[];
+    uint4(*slots)[4][kThreads] = reinterpret_cast<uint4(*)[4][kThreads]>(dyn);  // [stage][x0 x1 dy0 dy1]
+    float *factors = reinterpret_cast<float *>(dyn + sizeof(uint4) * kStages * 4 * kThreads);
+    __shared__ __align__(16) float sw[D];
+    pdl_trigger();  // the kernel that adds the weights' gradients up may take its place
     pdl_wait();
-    const int side = blockIdx.x >= a.nblk[0];
+    const int side = blockIdx.x >= a.nblk[0], tid = threadIdx.x;
     const unsigned blk = blockIdx.x - (side ? a.nblk[0] : 0);
     const int H = a.H[side];
-    const int li = threadIdx.x % LPR, g = threadIdx.x / LPR;
+    const int tl = tid % LPR, g = tid / LPR;
     const int p = g & ((1 << a.logP) - 1), h0 = g >> a.logP, HG = R >> a.logP;
-    const unsigned M = static_cast<unsigned>(a.B) * a.L, step = 1u << a.logP;
-    const long long hx = a.sx[side][1], hy = a.sy[side][1], hd = a.sdy[side][1];
-    const int pl = Rotation<LPR, VEC, INTER>::partner_lane(li, a.rot);
-    const int src = (threadIdx.x & 31 & ~(LPR - 1)) | pl;
-    float w[VEC], dw[VEC];
+    const int rounds = (H + HG - 1) / HG, size = 3 * N << a.logP;
+    const unsigned M = static_cast<unsigned>(a.B) * a.L;
+    const unsigned ntiles = (M + (1u << a.logP) - 1) >> a.logP, nblk = a.nblk[side];
+    const int mine = h0 < H ? (H - h0 + HG - 1) / HG : 0;  // this thread's rounds
+    int col[2];
+    lane_columns<LPR, VEC, INTER>(tl, a.rot, col);
+    // to the next round's head, and from a tile row to the thread's first one
+    const long long hx = a.sx[side][1] * HG, hy = a.sy[side][1] * HG, hd = a.sdy[side][1] * HG;
+    const long long first_x = a.sx[side][1] * h0, first_y = a.sy[side][1] * h0,
+                    first_d = a.sdy[side][1] * h0;
+
+    // the row to be fetched next: tile, round, and its address
+    unsigned ft = blk;
+    int fr = 0;
+    const T *fx = nullptr, *fd = nullptr;
+    auto fetch = [&](int stage) {
+        if (ft < ntiles) {
+            const unsigned m = (ft << a.logP) + p;
+            if (m < M) {
+                if (fr == 0) {
+                    const unsigned b = m / a.L, l = m - b * a.L;
+                    fx = static_cast<const T *>(a.x[side]) + b * a.sx[side][0] + l * a.sx[side][2] + first_x;
+                    fd = static_cast<const T *>(a.dy[side]) + b * a.sdy[side][0] + l * a.sdy[side][2] + first_d;
+                }
+                if (fr < mine) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        w[e] = a.w[side] ? a.w[side][li * VEC + e] : 1.f;
-        dw[e] = 0.f;
+                    for (int k = 0; k < 2; ++k) {
+                        cp_async16(&slots[stage][k][tid], fx + col[k]);
+                        cp_async16(&slots[stage][2 + k][tid], fd + col[k]);
+                    }
+                }
+                fx += hx;
+                fd += hd;
+            }
+            if (++fr == rounds) fr = 0, ft += nblk;
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    if (tid < D) sw[tid] = a.w[side] ? a.w[side][tid] : 1.f;
+    tile_factors<LPR, VEC, INTER>(a, blk << a.logP, M, factors);
+    __syncthreads();
+    float2 w[2][E], dw[2][E];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        load_weights<VEC>(sw, col[k], w[k]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) dw[k][e] = make_float2(0.f, 0.f);
     }
-    const unsigned ntiles = (M + step - 1) >> a.logP;
-    for (unsigned t = blk; t < ntiles; t += a.nblk[side]) {
-        const unsigned m0 = t << a.logP, m = m0 + p;
+    int stage = 0, buf = 0;
+    for (unsigned t = blk; t < ntiles; t += nblk) {
+        if (t + nblk < ntiles)
+            tile_factors<LPR, VEC, INTER>(a, (t + nblk) << a.logP, M, factors + (buf ^ 1) * size);
+        const float *row = factors + buf * size + p * 3 * N;
+        const unsigned m = (t << a.logP) + p;
         const bool live = m < M;
         const unsigned b = live ? m / a.L : 0, l = live ? m - b * a.L : 0;
-        const T *x = static_cast<const T *>(a.x[side]) + b * a.sx[side][0] + l * a.sx[side][2] + li * VEC;
-        const T *dy = static_cast<const T *>(a.dy[side]) + b * a.sdy[side][0] + l * a.sdy[side][2] + li * VEC;
-        T *dx = static_cast<T *>(a.y[side]) + b * a.sy[side][0] + l * a.sy[side][2] + li * VEC;
-        P vx[U], vd[U];
+        T *dx = static_cast<T *>(a.y[side]) + b * a.sy[side][0] + l * a.sy[side][2] + first_y;
+        for (int i = 0; i < rounds; ++i, dx += hy) {
+            fetch((stage + kStages - 1) % kStages);
+            cp_async_wait<kStages - 1>();
+            // rows past the end read a slot's old contents: they stay among their own lanes and
+            // nothing of them is kept
+            P v[2];
+            float2 d[2][E], f[2][E], c[E], s[E];
+            v[0].raw = slots[stage][2][tid];
+            v[1].raw = slots[stage][3][tid];
+            v[0].to(f[0]);
+            v[1].to(f[1]);
+            load_factors<LPR, VEC>(row, tl, c);
+            load_factors<LPR, VEC>(row + N, tl, s);
+            // dn, rotated back
+            if (INTER) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * HG;
-            const bool on = live && h < H;
-            vx[u] = on ? P::load(x + h * hx) : P::zero();
-            vd[u] = on ? P::load(dy + h * hd) : P::zero();
-        }
-        __syncthreads();  // the previous tile's angles are no longer read
-        tile_angles(a, m0, M, cs);
-        __syncthreads();
-        Rotation<LPR, VEC, INTER> rt;
-        if (live) rt.load(cs + p * (a.rot / 2), li, a.rot);
-        for (int h = h0; h - h0 < H; h += U * HG) {
+                for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int hu = h + u * HG, hn = hu + U * HG;
-                const bool on = live && hu < H;
-                float f[VEC], d[VEC], q[VEC], ss = 0.f, ux = 0.f;
-                vx[u].to(f);
-                vd[u].to(d);
-                partners<VEC, INTER>(vd[u], d, src, q);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    d[e] = fmaf(d[e], rt.c[e], -q[e] * rt.s[e]);  // dn: rotated back
-                    ss = fmaf(f[e], f[e], ss);
-                    ux = fmaf(d[e] * w[e], f[e], ux);
-                }
-                ss = row_sum<LPR>(ss);
-                ux = row_sum<LPR>(ux);
-                const float r = rsqrtf(ss * (1.f / D) + a.eps);
-                const float k = r * r * ux * (1.f / D);
-                if (on) {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        dw[e] = fmaf(d[e], f[e] * r, dw[e]);
-                        d[e] = r * fmaf(d[e], w[e], -f[e] * k);
+                    for (int e = 0; e < E; ++e) {
+                        const float se = of_pair<VEC>(s, k, e);
+                        d[k][e] = fma2(swapped(f[k][e]), make_float2(se, -se),
+                                       mul2(f[k][e], both(of_pair<VEC>(c, k, e))));
                     }
-                    P::from(d).store(dx + hu * hy);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) d[0][e] = fma2(f[1][e], s[e], mul2(f[0][e], c[e]));
+                load_factors<LPR, VEC>(row + 2 * N, tl, s);
+#pragma unroll
+                for (int e = 0; e < E; ++e) d[1][e] = fma2(f[0][e], s[e], mul2(f[1][e], c[e]));
+            }
+            v[0].raw = slots[stage][0][tid];
+            v[1].raw = slots[stage][1][tid];
+            v[0].to(f[0]);
+            v[1].to(f[1]);
+            stage = (stage + 1) % kStages;
+            float2 ss[2], ux[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                ss[k] = ux[k] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    ss[k] = fma2(f[k][e], f[k][e], ss[k]);
+                    ux[k] = fma2(mul2(d[k][e], w[k][e]), f[k][e], ux[k]);
                 }
-                if (live && hn < H) {
-                    vx[u] = P::load(x + hn * hx);
-                    vd[u] = P::load(dy + hn * hd);
+            }
+            ss[0] = add2(ss[0], ss[1]);
+            ux[0] = add2(ux[0], ux[1]);
+            const float s1 = row_sum<LPR>(ss[0].x + ss[0].y), s2 = row_sum<LPR>(ux[0].x + ux[0].y);
+            const float r = rsqrtf(s1 * (1.f / D) + a.eps);
+            const float q = -r * r * s2 * (1.f / D);
+            if (live && i < mine) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        f[k][e] = mul2(f[k][e], both(r));
+                        dw[k][e] = fma2(d[k][e], f[k][e], dw[k][e]);
+                        // r (u - x r^2 mean(u x)), u = dn w
+                        d[k][e] = fma2(f[k][e], both(q), mul2(mul2(d[k][e], w[k][e]), both(r)));
+                    }
+                    P::from(d[k]).store(dx + col[k]);
                 }
             }
         }
+        __syncthreads();  // the factors: this tile's are done with, the next one's are there
+        buf ^= 1;
     }
     if (!a.part) return;
     // the block's sums: R row groups over D columns, added in a fixed order
-    float *sum = reinterpret_cast<float *>(cs);
+    float *sum = reinterpret_cast<float *>(dyn);
+    cp_async_wait<0>();
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) sum[g * D + li * VEC + e] = dw[e];
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            reinterpret_cast<float2 *>(sum + g * D + col[k])[e] = dw[k][e];
     __syncthreads();
-    if (threadIdx.x < D) {
+    if (tid < D) {
         float s = 0.f;
-        for (int i = 0; i < R; ++i) s += sum[i * D + threadIdx.x];
-        a.part[static_cast<size_t>(blockIdx.x) * D + threadIdx.x] = s;
+        for (int i = 0; i < R; ++i) s += sum[i * D + tid];
+        a.part[static_cast<size_t>(blockIdx.x) * D + tid] = s;
     }
 }
 
 // dw[side][col] = sum over the side's blocks of their sums: grid (d / 32, side), 32 columns x
-// 8 slices of the blocks.
-__global__ void __launch_bounds__(256) qk_dw_kernel(const QkArgs a) {
-    __shared__ float sum[8][32];
+// 32 slices of the blocks.
+__global__ void __launch_bounds__(1024) qk_dw_kernel(const QkArgs a) {
+    __shared__ float sum[32][33];
     pdl_wait();
-    const int side = blockIdx.y, col = blockIdx.x * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
+    const int side = blockIdx.y, lane = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + lane;
     const int first = side ? a.nblk[0] : 0, n = a.nblk[side];
     float s = 0.f;
-    for (int i = y; i < n; i += 8) s += a.part[static_cast<size_t>(first + i) * a.d + col];
-    sum[y][threadIdx.x & 31] = s;
+#pragma unroll 8
+    for (int i = y; i < n; i += 32) s += a.part[static_cast<size_t>(first + i) * a.d + col];
+    sum[y][lane] = s;
     __syncthreads();
-    if (y == 0 && a.dw[side]) {
-        s = 0.f;
+    if (!a.dw[side]) return;
+    s = sum[lane][y];  // slice `lane` of column y
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += sum[i][threadIdx.x];
-        a.dw[side][col] = s;
-    }
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) a.dw[side][blockIdx.x * 32 + y] = s;
+}
+
+size_t bwd_smem(int d, int logP) {
+    return sizeof(uint4) * kStages * 4 * kThreads + size_t(4) * 2 * (3 * d / 2 << logP);
 }
 
 template <typename T, int LPR, bool INTER>
@@ -276,8 +405,8 @@ cudaError_t launch(const QkArgs &a, int backward, cudaStream_t st) {
     const unsigned tiles = (M + (1u << a.logP) - 1) >> a.logP;
     if (backward)
         return launch_pdl(qk_norm_bwd_kernel<T, LPR, INTER>, dim3(a.nblk[0] + a.nblk[1]),
-                          dim3(kThreads), 0, st, a);
-    return launch_pdl(qk_norm_kernel<T, LPR, INTER>, dim3(tiles, 2), dim3(kThreads), 0, st, a);
+                          dim3(kThreads), bwd_smem(a.d, a.logP), st, a);
+    return launch_pdl(qk_norm_kernel<T, 2 * LPR, INTER>, dim3(tiles, 2), dim3(kThreads), 0, st, a);
 }
 
 template <typename T, int LPR>
@@ -285,45 +414,72 @@ cudaError_t launch_i(const QkArgs &a, int backward, cudaStream_t st) {
     return a.inter ? launch<T, LPR, true>(a, backward, st) : launch<T, LPR, false>(a, backward, st);
 }
 
-// Rows per tile: the most, up to the row groups of a block, that still leave `want` tiles.
-int tile_log(unsigned M, int groups, unsigned want) {
+// Rows per tile (as a power of two): the most, up to `most`, that still leave `want` tiles.
+int tile_log(unsigned M, int most, unsigned want) {
     int k = 0;
-    while ((2 << k) <= groups && ((M >> (k + 1)) >= want)) ++k;
+    while ((2 << k) <= most && ((M >> (k + 1)) >= want)) ++k;
     return k;
+}
+
+template <typename T, int LPR>
+cudaError_t configure() {
+    const int smem = static_cast<int>(bwd_smem(LPR * 32 / sizeof(T), kQkMaxLogP));
+    const cudaError_t e = cudaFuncSetAttribute(qk_norm_bwd_kernel<T, LPR, false>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return e != cudaSuccess ? e
+                            : cudaFuncSetAttribute(qk_norm_bwd_kernel<T, LPR, true>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
 }  // namespace
 
-// Blocks of the backward kernel: four per SM, shared between the sides in the proportion of
-// their heads, at least one each.
+// Tiles of as many rows as leave every SM one: a tile's angles cost more than uneven ends do
+// (four tiles per SM: 13.8 us instead of 8.2 for 2048 rows of 16 + 16 heads of 128, forward; two
+// per SM: 15.2 instead of 10.4 for 2331 rows of 6 + 2 heads of 64, fp32, backward). The backward
+// pass takes at most 2^kQkMaxLogP rows, so that its blocks end together (32 rows: 77 us instead
+// of 70 for 16384 rows of 16 + 16 heads of 128), in kQkBlocksPerSm blocks per SM shared between
+// the sides in the proportion of their heads, at least one each.
 cudaError_t launch_qk_norm(QkArgs &a, int backward, int bf16, int num_sms, cudaStream_t st) {
-    const int vec = bf16 ? 8 : 4, lpr = a.d / vec, groups = kThreads / lpr;
+    const int vec = bf16 ? 8 : 4, lpr = a.d / (2 * vec), groups = kThreads / lpr;
     const unsigned M = static_cast<unsigned>(a.B) * a.L;
-    a.logP = tile_log(M, groups, 4u * num_sms);
     if (backward) {
+        const int most = groups < (1 << kQkMaxLogP) ? groups : 1 << kQkMaxLogP;
+        a.logP = tile_log(M, most, num_sms);
         const int total = kQkBlocksPerSm * (num_sms < kQkMaxSms ? num_sms : kQkMaxSms);
         int nq = static_cast<int>(static_cast<long long>(total) * a.H[0] / (a.H[0] + a.H[1]));
         nq = nq < 1 ? 1 : nq > total - 1 ? total - 1 : nq;
         const unsigned tiles = (M + (1u << a.logP) - 1) >> a.logP;
         a.nblk[0] = static_cast<unsigned>(nq) < tiles ? nq : static_cast<int>(tiles);
         a.nblk[1] = static_cast<unsigned>(total - nq) < tiles ? total - nq : static_cast<int>(tiles);
+    } else {
+        a.logP = tile_log(M, groups / 2, num_sms);
     }
     if (bf16) {
         switch (a.d) {
-            case 32: return launch_i<__nv_bfloat16, 4>(a, backward, st);
-            case 64: return launch_i<__nv_bfloat16, 8>(a, backward, st);
-            default: return launch_i<__nv_bfloat16, 16>(a, backward, st);
+            case 32: return launch_i<__nv_bfloat16, 2>(a, backward, st);
+            case 64: return launch_i<__nv_bfloat16, 4>(a, backward, st);
+            default: return launch_i<__nv_bfloat16, 8>(a, backward, st);
         }
     }
     switch (a.d) {
-        case 32: return launch_i<float, 8>(a, backward, st);
-        case 64: return launch_i<float, 16>(a, backward, st);
-        default: return launch_i<float, 32>(a, backward, st);
+        case 32: return launch_i<float, 4>(a, backward, st);
+        case 64: return launch_i<float, 8>(a, backward, st);
+        default: return launch_i<float, 16>(a, backward, st);
     }
 }
 
 cudaError_t launch_qk_dw(const QkArgs &a, cudaStream_t st) {
-    return launch_pdl(qk_dw_kernel, dim3(a.d / 32, 2), dim3(256), 0, st, a);
+    return launch_pdl(qk_dw_kernel, dim3(a.d / 32, 2), dim3(1024), 0, st, a);
+}
+
+cudaError_t qk_kernels_configure() {
+    cudaError_t e;
+    if ((e = configure<__nv_bfloat16, 2>()) != cudaSuccess ||
+        (e = configure<__nv_bfloat16, 4>()) != cudaSuccess ||
+        (e = configure<__nv_bfloat16, 8>()) != cudaSuccess ||
+        (e = configure<float, 4>()) != cudaSuccess || (e = configure<float, 8>()) != cudaSuccess)
+        return e;
+    return configure<float, 16>();
 }
 
 }  // namespace rsa

@@ -281,6 +281,7 @@ rsa_status_t device_state(DeviceState **out) {
             (e = rsa::bwd_kernels_configure()) != cudaSuccess ||
             (e = rsa::fwd_kernels_configure()) != cudaSuccess ||
             (e = rsa::linear_kernels_configure()) != cudaSuccess ||
+            (e = rsa::qk_kernels_configure()) != cudaSuccess ||
             (e = rsa::embed_kernels_configure()) != cudaSuccess)
             return cuda_fail("cudaFuncSetAttribute", e);
         void *ptr = nullptr;

@@ -130,7 +130,8 @@ cudaError_t linear_kernels_configure();
 
 // ---- row-local operators (kernels_qknorm.cu, kernels_embed.cu, kernels_distill.cu) ------------
 // Norm and rotation of queries (side 0) and keys (side 1). Strides: (batch, head, row).
-constexpr int kQkBlocksPerSm = 4, kQkMaxSms = 160;  // the backward kernel's blocks, at most
+constexpr int kQkBlocksPerSm = 2, kQkMaxSms = 160;  // the backward kernel's blocks, at most
+constexpr int kQkMaxLogP = 4;                       // its tiles: at most 16 rows
 struct QkArgs {
     const void *x[2], *dy[2];  // inputs; the outputs' gradients (backward)
     void *y[2];                // outputs; backward: the inputs' gradients
@@ -150,6 +151,7 @@ struct QkArgs {
 cudaError_t launch_qk_norm(QkArgs &a, int backward, int bf16, int num_sms, cudaStream_t st);
 // The weights' gradients from a.part, after the backward launch that set a.nblk.
 cudaError_t launch_qk_dw(const QkArgs &a, cudaStream_t st);
+cudaError_t qk_kernels_configure();
 
 struct EmbedArgs {
     const void *ids;

@@ -33,23 +33,26 @@ from . import rsa
 MAX_K = 1024  # RSA_DISTILL_MAX_K
 
 _INDEX = {torch.int64: 1, torch.int32: 0}
+_DT = {torch.bfloat16: rsa.RSA_BF16, torch.float32: rsa.RSA_F32}
+_S12, _S18 = ctypes.c_longlong * 12, ctypes.c_longlong * 18
 
 
 def _call(name, device, stream, tensors, body):
     """Runs ``body(lib, stream handle)`` with the tensors' device current and, where `stream` is
     not the current one, with its allocations made for `stream`. `body` returns the status code
     and the result."""
-    lib = rsa.load_library()
-    if device.index == torch.cuda.current_device() and stream is None:
-        rc, out = body(lib, torch.cuda.current_stream(device).cuda_stream)
+    lib = rsa._lib or rsa.load_library()
+    if stream is None and device.index == torch.cuda.current_device():
+        # the current stream's handle, without building a Stream object around it
+        rc, out = body(lib, torch._C._cuda_getCurrentRawStream(device.index))
     else:
-        s = stream if stream is not None else torch.cuda.current_stream(device)
+        here = torch.cuda.current_stream(device)
+        s = stream if stream is not None else here
         if s.device != device:
             raise ValueError(f"stream on {s.device}, expected {device} (the tensors' device)")
-        other = s != torch.cuda.current_stream(device)
         with torch.cuda.device(device), torch.cuda.stream(s):
             rc, out = body(lib, s.cuda_stream)
-        if other:
+        if s != here:
             for t in tensors:
                 if t is not None:
                     t.record_stream(s)
@@ -58,27 +61,26 @@ def _call(name, device, stream, tensors, body):
     return out
 
 
-def _on_gpu(*named):
+def _on_gpu(*tensors):
     """Tensors of one call live on one CUDA device; returns it."""
-    device = named[0][1].device
-    for name, t in named:
-        if t is not None:
-            if not t.is_cuda:
-                raise ValueError(f"{name} must be on a CUDA device")
-            if t.device != device:
-                raise ValueError(f"{name} is on {t.device}, expected {device}")
+    device = tensors[0].device
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, got {device}")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensor on {t.device}, expected {device} (the first tensor's device)")
     return device
 
 
 def _shaped(name, t, shape, dtype):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _given_workspace(workspace, device):
-    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+    if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {device}")
     return workspace
 
@@ -87,77 +89,70 @@ def _nbytes(t):
     return t.numel() * t.element_size()
 
 
-def _int32(**sizes):
+def _int32(*sizes):
     """Sizes that the library takes as 32-bit numbers."""
-    for name, n in sizes.items():
-        if not 0 <= n <= 0x7fffffff:
-            raise ValueError(f"{name} = {n} is outside [0, 2^31)")
+    if not 0 <= min(sizes) <= max(sizes) <= 0x7fffffff:
+        raise ValueError(f"a size among {sizes} is outside [0, 2^31)")
+
+
+def _dtype(t):
+    dt = _DT.get(t.dtype)
+    return rsa._dtype_code(t.dtype) if dt is None else dt  # which says what is wrong
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _like(t):
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 # ----------------------------------------------------------------- norm and rotation
 
 
-def _qk_checked(q, k, wq, wk, freq, positions, rest, outputs):
-    """Checks what both passes share; `rest` and `outputs` are (name, tensor or None, like q)."""
-    rsa._dtype_code(q.dtype)
+def _qk_checked(q, k, wq, wk, freq, positions, *same):
+    """Checks what both passes share; `same` are the tensors shaped like q and k in turn, or None.
+    Returns the device, the arguments from the frequencies to the type, and the tensors' strides
+    (those of outputs still to be allocated excepted)."""
+    dt = _dtype(q)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("queries and keys must be [B, heads, L, d]")
-    B, Hq, L, d = q.shape
+    qs, ks = q.shape, k.shape
+    B, Hq, L, d = qs
     if k.dtype != q.dtype:
         raise TypeError(f"keys must be {q.dtype}, got {k.dtype}")
-    if k.shape[0] != B or k.shape[2:] != q.shape[2:]:
+    if ks[0] != B or ks[2] != L or ks[3] != d:
         raise ValueError("queries and keys must agree in B, L and d")
-    _int32(B=B, Hq=Hq, Hk=k.shape[1], L=L, d=d)
-    device = _on_gpu(("q", q), ("k", k), ("wq", wq), ("wk", wk), ("freq", freq),
-                     ("positions", positions), *((n, t) for n, t, _ in rest + outputs))
-    for name, t, like_q in rest + outputs:
-        if t is not None:
-            _shaped(name, t, q.shape if like_q else k.shape, q.dtype)
-    for name, t in [("q", q), ("k", k)] + [(n, t) for n, t, _ in rest + outputs]:
-        if t is not None and not _vector_rows(t):
-            raise ValueError(f"{name}: rows must be contiguous and start on 16-byte boundaries")
-    for name, w in (("wq", wq), ("wk", wk)):
+    _int32(B, Hq, ks[1], L, d)
+    device = _on_gpu(q, k, wq, wk, freq, positions, *same)
+    for i, t in enumerate((q, k) + same):
+        if t is None:
+            continue
+        if i > 1:
+            _shaped("a tensor like the " + ("keys" if i & 1 else "queries"), t, ks if i & 1 else qs, q.dtype)
+        if t.stride(3) != 1 and d > 1:
+            raise ValueError("rows of d elements must be contiguous")
+    for w in (wq, wk):
         if w is not None:
-            _shaped(name, w, (d,), torch.float32)
+            _shaped("a norm's weight", w, (d,), torch.float32)
             if not w.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
+                raise ValueError("a norm's weight must be contiguous")
+    rot = 0
     if freq is not None:
         if freq.dtype != torch.float32 or freq.dim() != 1 or not freq.is_contiguous():
             raise ValueError("freq must be contiguous fp32 [rot / 2]")
-    pos_sb = 0
+        rot = 2 * freq.numel()
+    pos, pos64, pos_sb = None, 0, 0
     if positions is not None:
-        if positions.dtype not in _INDEX:
+        pos64 = _INDEX.get(positions.dtype)
+        if pos64 is None:
             raise TypeError("positions must be int64 or int32")
-        if tuple(positions.shape) not in ((L,), (B, L)) or (L > 1 and positions.stride(-1) != 1):
+        two = positions.dim() == 2
+        if positions.shape != ((B, L) if two else (L,)) or (L > 1 and positions.stride(-1) != 1):
             raise ValueError("positions must be [L] or [B, L] with contiguous rows")
-        pos_sb = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
-    return device, pos_sb
-
-
-def _vector_rows(t):
-    """Rows the kernels can read: contiguous, 16-byte aligned."""
-    if t.numel() == 0:
-        return True
-    vec = 16 // t.element_size()
-    shape, stride = t.shape, t.stride()
-    return (stride[-1] == 1 and t.data_ptr() % 16 == 0
-            and all(n == 1 or s % vec == 0 for n, s in zip(shape[:-1], stride[:-1])))
-
-
-def _strides(*ts):
-    return (ctypes.c_longlong * (3 * len(ts)))(*(s for t in ts for s in t.stride()[:3]))
-
-
-def _qk_tail(q, k, freq, positions, pos_sb, pos0, eps, interleaved):
-    B, Hq, L, d = q.shape
-    rot = 0 if freq is None else 2 * freq.numel()
-    return (_addr(freq), _addr(positions), _INDEX[positions.dtype] if positions is not None else 0,
-            pos_sb, int(pos0), B, Hq, k.shape[1], L, d, rot, int(bool(interleaved)), float(eps),
-            rsa._dtype_code(q.dtype))
+        pos, pos_sb = positions.data_ptr(), positions.stride(0) if two and B > 1 else 0
+    return device, (_addr(freq), pos, pos64, pos_sb), (B, Hq, ks[1], L, d, rot), dt
 
 
 def qk_norm_rope(q, k, wq, wk, freq, *, pos0: int = 0, positions=None, eps: float = 1e-6,
@@ -171,15 +166,15 @@ def qk_norm_rope(q, k, wq, wk, freq, *, pos0: int = 0, positions=None, eps: floa
     bf16 or fp32, d in {32, 64, 128}. Rows must be contiguous and 16-byte aligned, the other
     strides are free: views of the projection's output, or of the ring's key buffer as out_k.
     out_q=q, out_k=k work in place. Returns (q', k'), contiguous unless given."""
-    device, pos_sb = _qk_checked(q, k, wq, wk, freq, positions, [],
-                                 [("out_q", out_q, True), ("out_k", out_k, False)])
+    device, pos, sizes, dt = _qk_checked(q, k, wq, wk, freq, positions, out_q, out_k)
 
     def body(lib, s):
-        oq = torch.empty(q.shape, dtype=q.dtype, device=device) if out_q is None else out_q
-        ok = torch.empty(k.shape, dtype=k.dtype, device=device) if out_k is None else out_k
-        rc = lib.rsa_qk_norm_rope(_addr(q), _addr(k), _addr(oq), _addr(ok), _strides(q, k, oq, ok),
-                                  _addr(wq), _addr(wk),
-                                  *_qk_tail(q, k, freq, positions, pos_sb, pos0, eps, interleaved), s)
+        oq = _like(q) if out_q is None else out_q
+        ok = _like(k) if out_k is None else out_k
+        st = _S12(*q.stride()[:3], *k.stride()[:3], *oq.stride()[:3], *ok.stride()[:3])
+        rc = lib.rsa_qk_norm_rope(q.data_ptr(), k.data_ptr(), oq.data_ptr(), ok.data_ptr(), st,
+                                  _addr(wq), _addr(wk), *pos, pos0, *sizes, bool(interleaved),
+                                  eps, dt, s)
         return rc, (oq, ok)
 
     return _call("rsa_qk_norm_rope", device, stream, (q, k, wq, wk, freq, positions, out_q, out_k),
@@ -194,27 +189,26 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, wq, wk, freq, *, pos0: int = 0, 
     (dq, dk, dwq, dwk): dq, dk like q, k (dq=dq_out or dq=q work in place), dwq, dwk fp32 [d]
     (None where the weight is None, or without need_weights). The workspace, if given, holds
     ``qk_norm_rope_workspace_size(d)`` bytes."""
-    device, pos_sb = _qk_checked(q, k, wq, wk, freq, positions,
-                                 [("dq_out", dq_out, True), ("dk_out", dk_out, False)],
-                                 [("dq", dq, True), ("dk", dk, False)])
+    device, pos, sizes, dt = _qk_checked(q, k, wq, wk, freq, positions, dq_out, dk_out, dq, dk)
 
     def body(lib, s):
-        d = q.shape[3]
-        gq = torch.empty(q.shape, dtype=q.dtype, device=device) if dq is None else dq
-        gk = torch.empty(k.shape, dtype=k.dtype, device=device) if dk is None else dk
-        want = [w is not None and need_weights for w in (wq, wk)]
-        dws, ws = [None, None], None
-        if any(want):
-            n = lib.rsa_qk_norm_rope_workspace_size(d)
-            ws = (torch.empty(max(n, 256), dtype=torch.uint8, device=device) if workspace is None
-                  else _given_workspace(workspace, device))
-            dws = [torch.empty(d, dtype=torch.float32, device=device) if w else None for w in want]
+        d = sizes[4]
+        gq = _like(q) if dq is None else dq
+        gk = _like(k) if dk is None else dk
+        dwq = dwk = ws = None
+        if need_weights and (wq is not None or wk is not None):
+            ws = (torch.empty(max(lib.rsa_qk_norm_rope_workspace_size(d), 256), dtype=torch.uint8,
+                              device=device)
+                  if workspace is None else _given_workspace(workspace, device))
+            dwq = None if wq is None else torch.empty_like(wq)
+            dwk = None if wk is None else torch.empty_like(wk)
+        st = _S18(*q.stride()[:3], *k.stride()[:3], *dq_out.stride()[:3], *dk_out.stride()[:3],
+                  *gq.stride()[:3], *gk.stride()[:3])
         rc = lib.rsa_qk_norm_rope_backward(
-            _addr(q), _addr(k), _addr(dq_out), _addr(dk_out), _addr(gq), _addr(gk),
-            _strides(q, k, dq_out, dk_out, gq, gk), _addr(wq), _addr(wk), _addr(dws[0]),
-            _addr(dws[1]), *_qk_tail(q, k, freq, positions, pos_sb, pos0, eps, interleaved),
-            _addr(ws), 0 if ws is None else _nbytes(ws), s)
-        return rc, (gq, gk, dws[0], dws[1])
+            q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), gq.data_ptr(),
+            gk.data_ptr(), st, _addr(wq), _addr(wk), _addr(dwq), _addr(dwk), *pos, pos0, *sizes,
+            bool(interleaved), eps, dt, _addr(ws), 0 if ws is None else _nbytes(ws), s)
+        return rc, (gq, gk, dwq, dwk)
 
     return _call("rsa_qk_norm_rope_backward", device, stream,
                  (q, k, dq_out, dk_out, wq, wk, freq, positions, dq, dk, workspace), body)
@@ -226,6 +220,15 @@ def qk_norm_rope_workspace_size(d: int) -> int:
     if n == 0:
         raise rsa.RSAError(rsa.RSA_ERR_UNSUPPORTED, "rsa_qk_norm_rope_workspace_size")
     return int(n)
+
+
+def _vector_rows(t):
+    """Rows the kernels can read: contiguous, 16-byte aligned."""
+    if t.numel() == 0:
+        return True
+    vec = 16 // t.element_size()
+    return (t.stride(-1) == 1 and t.data_ptr() % 16 == 0
+            and all(n == 1 or s % vec == 0 for n, s in zip(t.shape[:-1], t.stride()[:-1])))
 
 
 class QKNormRope(torch.autograd.Function):
@@ -255,11 +258,12 @@ class QKNormRope(torch.autograd.Function):
 
 
 def _ids_checked(ids):
-    if ids.dtype not in _INDEX:
+    i64 = _INDEX.get(ids.dtype)
+    if i64 is None:
         raise TypeError("ids must be int64 or int32")
     if not ids.is_contiguous():
         raise ValueError("ids must be contiguous")
-    return _INDEX[ids.dtype]
+    return i64
 
 
 def _ld(t):
@@ -283,23 +287,22 @@ def embed(ids, table, scale: float = 1.0, *, out=None, stream: torch.cuda.Stream
     """``scale * table[ids]``: ids int64 or int32 of any shape, table [V, D] bf16 or fp32 (rows
     contiguous, any distance apart). An id outside [0, V) gives a row of zeros. Returns
     [*ids.shape, D] in the table's type."""
-    i64 = _ids_checked(ids)
-    dt = rsa._dtype_code(table.dtype)
+    i64, dt, n = _ids_checked(ids), _dtype(table), ids.numel()
     if table.dim() != 2:
         raise ValueError("table must be [V, D]")
     V, D = table.shape
-    _int32(V=V, D=D, tokens=ids.numel())
-    device = _on_gpu(("table", table), ("ids", ids), ("out", out))
+    _int32(V, D, n)
+    device = _on_gpu(table, ids, out)
     shape = (*ids.shape, D)
     if out is not None:
         _shaped("out", out, shape, table.dtype)
     ld = _ld(table)
 
     def body(lib, s):
-        o = torch.empty(shape, dtype=table.dtype, device=device) if out is None else out
-        flat = o if o.dim() == 2 else _flat("out", o, D)
-        rc = lib.rsa_embed(_addr(ids), i64, _addr(table), ld, _addr(flat), _ld(flat), ids.numel(),
-                           V, D, float(scale), dt, s)
+        o = table.new_empty(shape) if out is None else out
+        ldo = D if out is None else _ld(_flat("out", o, D))
+        rc = lib.rsa_embed(ids.data_ptr(), i64, table.data_ptr(), ld, o.data_ptr(), ldo, n, V, D,
+                           scale, dt, s)
         return rc, o
 
     return _call("rsa_embed", device, stream, (ids, table, out), body)
@@ -312,15 +315,14 @@ def embed_backward(ids, dout, num_rows: int, scale: float = 1.0, *, dtable=None,
     summed by id in fp32, times scale. The order of the sums is fixed. dtable: where it goes,
     in dout's type or fp32; with accumulate it is added to, and rows without a token are left as
     they are. The workspace, if given, holds ``embed_workspace_size`` bytes."""
-    i64 = _ids_checked(ids)
-    dt = rsa._dtype_code(dout.dtype)
-    if tuple(dout.shape[:-1]) != tuple(ids.shape) or dout.dim() < 1:
+    i64, dt, n = _ids_checked(ids), _dtype(dout), ids.numel()
+    if dout.dim() < 1 or dout.shape[:-1] != ids.shape:
         raise ValueError("dout must be [*ids.shape, D]")
     if accumulate and dtable is None:
         raise ValueError("accumulate needs the table's gradient to add to")
     V, D = int(num_rows), dout.shape[-1]
-    _int32(num_rows=V, D=D, tokens=ids.numel())
-    device = _on_gpu(("dout", dout), ("ids", ids), ("dtable", dtable))
+    _int32(V, D, n)
+    device = _on_gpu(dout, ids, dtable)
     if dtable is not None:
         _shaped("dtable", dtable, (V, D),
                 torch.float32 if dtable.dtype == torch.float32 else dout.dtype)
@@ -328,13 +330,14 @@ def embed_backward(ids, dout, num_rows: int, scale: float = 1.0, *, dtable=None,
     ld = _ld(g)
 
     def body(lib, s):
-        dtab = torch.empty((V, D), dtype=dout.dtype, device=device) if dtable is None else dtable
-        n = lib.rsa_embed_workspace_size(ids.numel(), V, D)
-        ws = (torch.empty(max(n, 256), dtype=torch.uint8, device=device) if workspace is None
-              else _given_workspace(workspace, device))
-        rc = lib.rsa_embed_backward(_addr(ids), i64, _addr(g), ld, _addr(dtab), _ld(dtab),
-                                    ids.numel(), V, D, float(scale), int(bool(accumulate)), dt,
-                                    rsa._dtype_code(dtab.dtype), _addr(ws), _nbytes(ws), s)
+        dtab = dout.new_empty((V, D)) if dtable is None else dtable
+        ws = (torch.empty(max(lib.rsa_embed_workspace_size(n, V, D), 256), dtype=torch.uint8,
+                          device=device)
+              if workspace is None else _given_workspace(workspace, device))
+        rc = lib.rsa_embed_backward(ids.data_ptr(), i64, g.data_ptr(), ld, dtab.data_ptr(),
+                                    D if dtable is None else _ld(dtab), n, V, D, scale,
+                                    bool(accumulate), dt, _DT[dtab.dtype], ws.data_ptr(),
+                                    _nbytes(ws), s)
         return rc, dtab
 
     return _call("rsa_embed_backward", device, stream, (ids, dout, dtable, workspace), body)
@@ -342,7 +345,7 @@ def embed_backward(ids, dout, num_rows: int, scale: float = 1.0, *, dtable=None,
 
 def embed_workspace_size(n: int, num_rows: int, D: int) -> int:
     """Workspace bytes of ``embed_backward`` for n tokens (0: none needed)."""
-    _int32(n=n, num_rows=num_rows, D=D)
+    _int32(int(n), int(num_rows), int(D))
     return int(rsa.load_library().rsa_embed_workspace_size(int(n), int(num_rows), int(D)))
 
 
@@ -365,36 +368,45 @@ class Embedding(torch.autograd.Function):
 # ----------------------------------------------------------------- distillation
 
 
-def _distill_checked(logits, index, teacher, temperature, rest):
-    dt, tdt = rsa._dtype_code(logits.dtype), rsa._dtype_code(teacher.dtype)
-    if index.dtype not in _INDEX:
+def _distill_checked(logits, index, teacher, temperature, *more):
+    dt, tdt, i64 = _dtype(logits), _dtype(teacher), _INDEX.get(index.dtype)
+    if i64 is None:
         raise TypeError("index must be int64 or int32")
-    if logits.dim() < 2 or index.dim() != logits.dim() or index.shape[:-1] != logits.shape[:-1]:
+    shape = logits.shape
+    if len(shape) < 2 or index.dim() != len(shape) or index.shape[:-1] != shape[:-1]:
         raise ValueError("logits [..., V] and index [..., K] must agree in their rows")
     if teacher.shape != index.shape:
         raise ValueError("teacher must have index's shape [..., K]")
     if not index.is_contiguous() or not teacher.is_contiguous():
         raise ValueError("index and teacher must be contiguous")
-    device = _on_gpu(("logits", logits), ("index", index), ("teacher", teacher), *rest)
-    V, K = logits.shape[-1], index.shape[-1]
+    device = _on_gpu(logits, index, teacher, *more)
+    V, K = shape[-1], index.shape[-1]
     z = _flat("logits", logits, V)
-    _int32(rows=z.shape[0], V=V, K=K)
-    return device, z, (z.shape[0], V, K, float(temperature), dt), (_INDEX[index.dtype], tdt)
+    n = z.shape[0]
+    _int32(n, V, K)
+    head = (z.data_ptr(), _ld(z), index.data_ptr(), i64, teacher.data_ptr(), tdt)
+    return device, shape[:-1], head, (n, V, K, temperature, dt)
 
 
 def _rows_of(name, t, shape):
-    """fp32 values of the rows, as (tensor, stride 0 or 1): a tensor of the rows' shape, an
-    expanded one, or a single value for all rows."""
+    """fp32 values of the rows: 1 (elements apart) for a contiguous tensor of the rows' shape, 0
+    for an expanded one or a single value for all rows."""
     if t.dtype != torch.float32:
         raise TypeError(f"{name} must be fp32, got {t.dtype}")
-    if t.dim() == 0 or all(n == 1 or s == 0 for n, s in zip(t.shape, t.stride())):
-        if t.dim() and tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must have shape {tuple(shape)} or be a single value")
-        return 0
-    _shaped(name, t, shape, torch.float32)
-    if not t.is_contiguous():
+    if t.dim() and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} or be a single value")
+    if t.dim() and t.is_contiguous():
+        return 1
+    if any(n > 1 and s != 0 for n, s in zip(t.shape, t.stride())):
         raise ValueError(f"{name} must be contiguous or one value expanded")
-    return 1
+    return 0
+
+
+def _given_rows(name, t, shape):
+    if t is not None:
+        _shaped(name, t, shape, torch.float32)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
 
 
 def distill(logits, index, teacher, temperature: float = 1.0, *, loss=None, stats=None,
@@ -403,57 +415,43 @@ def distill(logits, index, teacher, temperature: float = 1.0, *, loss=None, stat
     largest logits: index [..., K] (int64 or int32; outside [0, V): an empty slot) and teacher
     [..., K] (bf16 or fp32; -inf: an empty slot). With p = softmax(teacher / temperature) over the
     slots and q = softmax(logits / temperature): temperature^2 * sum p (ln p - ln q). A row of
-    empty slots has loss 0. With K = 1 this is the cross entropy with index as the label.
-    Returns (loss [...] fp32, stats [..., 2] fp32 = (max logit, ln sum exp((z - max) / T)))."""
-    device, z, sizes, kinds = _distill_checked(logits, index, teacher, temperature,
-                                               [("loss", loss), ("stats", stats)])
-    shape = logits.shape[:-1]
-    for name, t, sh in (("loss", loss, shape), ("stats", stats, (*shape, 2))):
-        if t is not None:
-            _shaped(name, t, sh, torch.float32)
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-    ld = _ld(z)
+    empty slots has loss 0. With K = 1 this is the cross entropy with index as the label, times
+    temperature^2. Returns (loss [...] fp32, stats [..., 2] fp32 = (max logit,
+    ln sum exp((z - max) / temperature)))."""
+    device, shape, head, sizes = _distill_checked(logits, index, teacher, temperature, loss, stats)
+    _given_rows("loss", loss, shape)
+    _given_rows("stats", stats, (*shape, 2))
 
     def body(lib, s):
         lo = torch.empty(shape, dtype=torch.float32, device=device) if loss is None else loss
-        sa = torch.empty((*shape, 2), dtype=torch.float32, device=device) if stats is None else stats
-        rc = lib.rsa_distill(_addr(z), ld, _addr(index), kinds[0], _addr(teacher), kinds[1],
-                             _addr(lo), _addr(sa), *sizes, s)
-        return rc, (lo, sa)
+        sa = lo.new_empty((*shape, 2)) if stats is None else stats
+        return lib.rsa_distill(*head, lo.data_ptr(), sa.data_ptr(), *sizes, s), (lo, sa)
 
     return _call("rsa_distill", device, stream, (logits, index, teacher, loss, stats), body)
 
 
-def _dlogits(logits, z, dlogits, device):
-    """The gradient's tensor and its [rows, V] view: the given one, or a new one."""
+def _gradient(logits, dlogits):
+    """The gradient's tensor, its address and the distance of its rows."""
     if dlogits is None:
-        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=device)
-    return dlogits, _flat("dlogits", dlogits, z.shape[1])
+        out = _like(logits)
+        return out, out.data_ptr(), out.shape[-1]
+    _shaped("dlogits", dlogits, logits.shape, logits.dtype)
+    return dlogits, dlogits.data_ptr(), _ld(_flat("dlogits", dlogits, dlogits.shape[-1]))
 
 
 def distill_backward(logits, index, teacher, stats, dloss, temperature: float = 1.0, *,
                      dlogits=None, stream: torch.cuda.Stream | None = None):
     """Gradient of ``distill``'s logits, dloss * temperature * (q - p), from its stats. dloss:
     fp32, of the rows' shape, or a single value for all rows. dlogits=logits works in place."""
-    device, z, sizes, kinds = _distill_checked(logits, index, teacher, temperature,
-                                               [("stats", stats), ("dloss", dloss),
-                                                ("dlogits", dlogits)])
-    shape = logits.shape[:-1]
-    _shaped("stats", stats, (*shape, 2), torch.float32)
-    if not stats.is_contiguous():
-        raise ValueError("stats must be contiguous")
+    device, shape, head, sizes = _distill_checked(logits, index, teacher, temperature, stats,
+                                                  dloss, dlogits)
+    _given_rows("stats", stats, (*shape, 2))
     step = _rows_of("dloss", dloss, shape)
-    if dlogits is not None:
-        _shaped("dlogits", dlogits, logits.shape, logits.dtype)
-    ld = _ld(z)
 
     def body(lib, s):
-        out, flat = _dlogits(logits, z, dlogits, device)
-        rc = lib.rsa_distill_backward(_addr(z), ld, _addr(index), kinds[0], _addr(teacher),
-                                      kinds[1], _addr(stats), _addr(dloss), step, _addr(flat),
-                                      _ld(flat), *sizes, s)
-        return rc, out
+        out, at, ld = _gradient(logits, dlogits)
+        return lib.rsa_distill_backward(*head, stats.data_ptr(), dloss.data_ptr(), step, at, ld,
+                                        *sizes, s), out
 
     return _call("rsa_distill_backward", device, stream,
                  (logits, index, teacher, stats, dloss, dlogits), body)
@@ -464,25 +462,16 @@ def distill_step(logits, index, teacher, dloss, temperature: float = 1.0, *, los
     """``distill`` and ``distill_backward`` in one pass over the logits, for a training loop that
     knows the rows' weights dloss beforehand (a mean's 1 / rows). Returns (loss, dlogits);
     dlogits=logits replaces the logits."""
-    device, z, sizes, kinds = _distill_checked(logits, index, teacher, temperature,
-                                               [("dloss", dloss), ("loss", loss),
-                                                ("dlogits", dlogits)])
-    shape = logits.shape[:-1]
+    device, shape, head, sizes = _distill_checked(logits, index, teacher, temperature, dloss, loss,
+                                                  dlogits)
+    _given_rows("loss", loss, shape)
     step = _rows_of("dloss", dloss, shape)
-    if loss is not None:
-        _shaped("loss", loss, shape, torch.float32)
-        if not loss.is_contiguous():
-            raise ValueError("loss must be contiguous")
-    if dlogits is not None:
-        _shaped("dlogits", dlogits, logits.shape, logits.dtype)
-    ld = _ld(z)
 
     def body(lib, s):
         lo = torch.empty(shape, dtype=torch.float32, device=device) if loss is None else loss
-        out, flat = _dlogits(logits, z, dlogits, device)
-        rc = lib.rsa_distill_step(_addr(z), ld, _addr(index), kinds[0], _addr(teacher), kinds[1],
-                                  _addr(dloss), step, _addr(lo), _addr(flat), _ld(flat), *sizes, s)
-        return rc, (lo, out)
+        out, at, ld = _gradient(logits, dlogits)
+        return lib.rsa_distill_step(*head, dloss.data_ptr(), step, lo.data_ptr(), at, ld, *sizes,
+                                    s), (lo, out)
 
     return _call("rsa_distill_step", device, stream,
                  (logits, index, teacher, dloss, loss, dlogits), body)
