@@ -282,7 +282,8 @@ rsa_status_t device_state(DeviceState **out) {
             (e = rsa::fwd_kernels_configure()) != cudaSuccess ||
             (e = rsa::linear_kernels_configure()) != cudaSuccess ||
             (e = rsa::qk_kernels_configure()) != cudaSuccess ||
-            (e = rsa::embed_kernels_configure()) != cudaSuccess)
+            (e = rsa::embed_kernels_configure()) != cudaSuccess ||
+            (e = rsa::distill_kernels_configure()) != cudaSuccess)
             return cuda_fail("cudaFuncSetAttribute", e);
         void *ptr = nullptr;
         e = cudaGetSymbolAddress(&ptr, rsa::g_status_word);

@@ -191,10 +191,12 @@ struct DistillArgs {
     void *dz;
     int n, V, K;
     float tau;
-    int cluster;  // CTAs per row, set by the launch
+    int log_cluster;  // CTAs per row, set by the launch
+    int ring;         // batches of a thread with a place in shared memory, likewise
 };
 // mode: 0 loss and statistics, 1 gradient, 2 loss and gradient.
 cudaError_t launch_distill(DistillArgs a, int mode, int bf16, int num_sms, cudaStream_t st);
+cudaError_t distill_kernels_configure();
 
 // ---- CUDA-core kernels (kernels_simt.cu) -----------------------------------------------
 // Row softmax of the group's fp32 slab, in place: P written as bf16 (p_bf16 = 1) into the
