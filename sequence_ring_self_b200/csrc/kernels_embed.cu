@@ -63,40 +63,51 @@ __global__ void __launch_bounds__(kLookupThreads) embed_kernel(const EmbedArgs a
 
 // ------------------------------------------------------------------ sort by id
 
-constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortCluster = 8;
-constexpr int kSortMaxBits = 10;  // digits: 32 warps x 1024 counters = 128 KB
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
+constexpr int kSortMaxBits = 9;  // digits: one per thread; 16 warps x 512 counters = 32 KB
+
+constexpr int kSortKeep = 4;  // rounds of 32 tokens that a warp loads at once
 
 // Stable LSD radix sort of the n (id, token) pairs by one cluster, any n: each warp of the
 // cluster owns a contiguous run of tokens; per pass it counts its digits (32 tokens at a time,
-// equal digits found by a match over the warp), the cluster adds the counts up over warps,
+// equal digits found by a ballot per bit; __match_any_sync took twice as long), the cluster adds the counts up over warps,
 // CTAs and digits through distributed shared memory, and the warps place their tokens in
 // order. The lists lie in global memory (in practice in L2); the cluster's barriers order the
-// passes. Ids outside [0, V) become V and sort last. The other clusters of the grid meanwhile
-// fill the table's gradient with zeros.
+// passes. Ids outside [0, V) become V and sort last. Bound by latency: about five dependent trips
+// to L2 or a neighbouring SM per pass (10 us for 16384 tokens).
+//
+// Unless the sums are added to what is there, the grid has more clusters, which meanwhile fill the
+// gradient with zeros in accesses of N elements, a row per warp (as a kernel of its own beside
+// the sort's this was no use: the cluster waits for SMs without other work).
 template <typename TO, int N>
-__global__ void __cluster_dims__(kSortCluster, 1, 1) __launch_bounds__(kSortThreads, 1)
-    embed_sort_kernel(const EmbedArgs a) {
+__global__ void __launch_bounds__(kSortThreads, 2) embed_sort_kernel(const EmbedArgs a) {
     pdl_wait();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (blockIdx.x >= kSortCluster) {
-        const unsigned nu = a.D / N;
-        const unsigned stride = (gridDim.x - kSortCluster) * kSortWarps;
-        for (unsigned r = (blockIdx.x - kSortCluster) * kSortWarps + warp;
+    pdl_trigger();
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = static_cast<int>(cluster.block_rank()), nc = a.sort_ctas;
+    if (blockIdx.x >= static_cast<unsigned>(nc)) {
+        const unsigned nu = a.D / N, stride = (gridDim.x - nc) * kSortWarps;
+        for (unsigned r = (blockIdx.x - nc) * kSortWarps + (threadIdx.x >> 5);
              r < static_cast<unsigned>(a.V); r += stride) {
             TO *row = static_cast<TO *>(a.dtable) + r * a.ld_dtable;
-            for (unsigned c = lane; c < nu; c += 32) Pack<TO, N>::zero().store(row + c * N);
+            for (unsigned c = threadIdx.x & 31; c < nu; c += 32) Pack<TO, N>::zero().store(row + c * N);
         }
         return;
     }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     extern __shared__ uint32_t cnt[];  // [warps][digits], then total[digits], base[digits]
     __shared__ uint32_t wsum[kSortWarps];
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = static_cast<int>(cluster.block_rank());
+    auto sync_all = [&]() {
+        if (nc > 1)
+            cluster.sync();
+        else
+            __syncthreads();
+    };
     const int nd = 1 << a.bits;
     uint32_t *mine = cnt + warp * nd, *total = cnt + kSortWarps * nd, *base = total + nd;
     if (rank == 0 && tid == 0) *a.count = 0;
     // per-warp runs of whole 32-token rounds
-    const unsigned n = a.n, all = kSortCluster * kSortThreads;
+    const unsigned n = a.n, all = nc * kSortThreads;
     const unsigned run = (n + all - 1) / all * 32;
     const unsigned long long s0 = static_cast<unsigned long long>(rank * kSortWarps + warp) * run;
     const unsigned start = s0 < n ? static_cast<unsigned>(s0) : n;
@@ -108,19 +119,48 @@ __global__ void __cluster_dims__(kSortCluster, 1, 1) __launch_bounds__(kSortThre
         const uint32_t *key_in = a.key[to ^ 1], *idx_in = a.idx[to ^ 1];
         uint32_t *key_out = a.key[to], *idx_out = a.idx[to];
         const int shift = pass * a.bits;
-        auto key_of = [&](unsigned t) -> uint32_t {
-            if (pass) return key_in[t];
-            const long long id = index_at(a.ids, a.ids64, t);
-            return id >= 0 && id < a.V ? static_cast<uint32_t>(id) : static_cast<uint32_t>(a.V);
+        uint32_t key[kSortKeep], idx[kSortKeep], peers[kSortKeep];
+        auto load = [&](unsigned t0) {
+#pragma unroll
+            for (int k = 0; k < kSortKeep; ++k) {
+                const unsigned t = t0 + k * 32 + lane;
+                key[k] = idx[k] = 0;
+                if (t >= end) continue;
+                // through L2: other SMs wrote the lists
+                if (pass) {
+                    key[k] = __ldcg(key_in + t);
+                    idx[k] = __ldcg(idx_in + t);
+                } else {
+                    const long long id = index_at(a.ids, a.ids64, t);
+                    key[k] = id >= 0 && id < a.V ? static_cast<uint32_t>(id) : static_cast<uint32_t>(a.V);
+                    idx[k] = t;
+                }
+            }
         };
+        auto digit = [&](int k) { return (key[k] >> shift) & (nd - 1); };
+        // the lanes with a token of the same digit; 0 for a lane without one
+        auto match = [&](unsigned t0, int k) {
+            const bool on = t0 + k * 32 + lane < end;
+            uint32_t same = __ballot_sync(0xffffffffu, on);
+            for (int b = 0; b < a.bits; ++b) {
+                const bool one = digit(k) >> b & 1;
+                const uint32_t ones = __ballot_sync(0xffffffffu, one);
+                same &= one ? ones : ~ones;
+            }
+            return on ? same : 0u;
+        };
+        load(start);
         for (int i = tid; i < kSortWarps * nd; i += kSortThreads) cnt[i] = 0;
         __syncthreads();
-        for (unsigned t0 = start; t0 < end; t0 += 32) {
-            const bool on = t0 + lane < end;
-            const uint32_t dig = on ? (key_of(t0 + lane) >> shift) & (nd - 1) : ~0u;
-            const uint32_t peers = __match_any_sync(0xffffffffu, dig);
-            if (on && !(peers & below)) mine[dig] += __popc(peers);
-            __syncwarp();
+        for (unsigned t0 = start; t0 < end; t0 += 32 * kSortKeep) {
+            if (t0 != start) load(t0);
+#pragma unroll
+            for (int k = 0; k < kSortKeep; ++k) {
+                if (t0 + k * 32 >= end) break;  // the whole warp
+                peers[k] = match(t0, k);
+                if (peers[k] && !(peers[k] & below)) mine[digit(k)] += __popc(peers[k]);
+                __syncwarp();
+            }
         }
         __syncthreads();
         if (tid < nd) {  // counts -> first place of each warp inside the CTA's share of a digit
@@ -133,11 +173,11 @@ __global__ void __cluster_dims__(kSortCluster, 1, 1) __launch_bounds__(kSortThre
             }
             total[tid] = s;
         }
-        cluster.sync();
+        sync_all();
         uint32_t before = 0, sum = 0;
         if (tid < nd) {
-#pragma unroll
-            for (int c = 0; c < kSortCluster; ++c) {
+#pragma unroll 4
+            for (int c = 0; c < nc; ++c) {
                 const uint32_t v = cluster.map_shared_rank(total, c)[tid];
                 before += c < rank ? v : 0;
                 sum += v;
@@ -153,40 +193,43 @@ __global__ void __cluster_dims__(kSortCluster, 1, 1) __launch_bounds__(kSortThre
         if (lane == 31) wsum[warp] = inc;
         __syncthreads();
         if (warp == 0) {
-            uint32_t v = wsum[lane], w = v;
+            uint32_t v = lane < kSortWarps ? wsum[lane] : 0, w = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint32_t x = __shfl_up_sync(0xffffffffu, w, o);
                 if (lane >= o) w += x;
             }
-            wsum[lane] = w - v;
+            if (lane < kSortWarps) wsum[lane] = w - v;
         }
         __syncthreads();
         if (tid < nd) base[tid] = wsum[warp] + inc - sum + before;
         __syncthreads();
-        for (unsigned t0 = start; t0 < end; t0 += 32) {
-            const unsigned t = t0 + lane;
-            const bool on = t < end;
-            const uint32_t key = on ? key_of(t) : 0;
-            const uint32_t dig = on ? (key >> shift) & (nd - 1) : ~0u;
-            const uint32_t peers = __match_any_sync(0xffffffffu, dig);
-            if (on) {
-                const uint32_t at = base[dig] + mine[dig] + __popc(peers & below);
-                key_out[at] = key;
-                idx_out[at] = pass ? idx_in[t] : t;
+        const bool kept = end - start <= 32 * kSortKeep;  // the tokens are still in registers
+        for (unsigned t0 = start; t0 < end; t0 += 32 * kSortKeep) {
+            if (!kept) load(t0);
+#pragma unroll
+            for (int k = 0; k < kSortKeep; ++k) {
+                if (t0 + k * 32 >= end) break;
+                if (!kept) peers[k] = match(t0, k);
+                const uint32_t dig = digit(k);
+                if (peers[k]) {
+                    const uint32_t at = base[dig] + mine[dig] + __popc(peers[k] & below);
+                    key_out[at] = key[k];
+                    idx_out[at] = idx[k];
+                }
+                __syncwarp();
+                if (peers[k] && !(peers[k] & below)) mine[dig] += __popc(peers[k]);
+                __syncwarp();
             }
-            __syncwarp();
-            if (on && !(peers & below)) mine[dig] += __popc(peers);
-            __syncwarp();
         }
         // this pass's lists are whole, and nobody reads this CTA's totals any more
-        cluster.sync();
+        sync_all();
     }
 }
 
 // ------------------------------------------------------------------ sums of the sorted rows
 
-constexpr int kGradUnroll = 8;
+constexpr int kGradUnroll = 4;  // rows of a batch; one batch is read ahead
 
 // N sums of row `key` of the table's gradient, from column col: scaled, added to what is there
 // when asked to, rounded once.
@@ -224,44 +267,56 @@ __device__ __forceinline__ void store_part(float *p, const float (&s)[N]) {
 // Block (x: columns of N elements, y: pieces). A piece's first id may have begun before it
 // (partial row 0) and its last may go on behind it (partial row 1, when it began inside).
 template <typename T, typename TO, int N>
-__global__ void __launch_bounds__(256) embed_grad_kernel(const EmbedArgs a) {
+__global__ void __launch_bounds__(256, 4) embed_grad_kernel(const EmbedArgs a) {
     using P = Pack<T, N>;
+    __shared__ uint32_t skey[256 + 2], sidx[256];
     pdl_wait();
-    const unsigned piece = blockIdx.x * blockDim.y + threadIdx.y;
+    pdl_trigger();
+    const unsigned piece0 = blockIdx.x * blockDim.y, S = a.S, n = a.n;
+    const uint32_t V = a.V;
+    // the block's stretch of the sorted lists, with the ids before and behind it
+    const unsigned first = piece0 * S, count = min(n - first, blockDim.y * S);
+    for (unsigned i = threadIdx.y * blockDim.x + threadIdx.x; i < count; i += blockDim.x * blockDim.y) {
+        skey[i + 1] = a.key[0][first + i];
+        sidx[i] = a.idx[0][first + i];
+    }
+    if (threadIdx.x == 0 && threadIdx.y == 0) {
+        skey[0] = first ? a.key[0][first - 1] : ~0u;
+        skey[count + 1] = first + count < n ? a.key[0][first + count] : ~0u;
+    }
+    __syncthreads();
+    const unsigned piece = piece0 + threadIdx.y;
     const int unit = blockIdx.y * blockDim.x + threadIdx.x;
     if (piece >= static_cast<unsigned>(a.npieces) || unit * N >= a.D) return;
     const int col = unit * N;
-    const uint32_t *key = a.key[0], *idx = a.idx[0];
-    const unsigned begin = piece * static_cast<unsigned>(a.S), n = a.n;
-    const unsigned end = n - begin < static_cast<unsigned>(a.S) ? n : begin + a.S;
+    const unsigned begin = threadIdx.y * S, end = min(begin + S, count);  // of the stretch
+    const uint32_t *key = skey + 1;
     const T *dout = static_cast<const T *>(a.dout) + col;
     float *part = a.part + static_cast<size_t>(piece) * 2 * a.Dp + col;
-    const uint32_t V = a.V;
 
     float s[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) s[e] = 0.f;
     uint32_t cur = key[begin];
-    bool began = begin == 0 || key[begin - 1] != cur;  // cur's first token lies in this piece
-    for (unsigned i0 = begin; i0 < end; i0 += kGradUnroll) {
-        uint32_t k[kGradUnroll];
-        P v[kGradUnroll];
+    bool began = skey[begin] != cur;  // cur's first token lies in this piece
+    auto load = [&](P(&v)[kGradUnroll], unsigned i0) {
 #pragma unroll
         for (int u = 0; u < kGradUnroll; ++u) {
             const unsigned i = i0 + u;
-            k[u] = i < end ? key[i] : V;
-            v[u] = k[u] < V ? P::load(dout + idx[i] * a.ld_dout) : P::zero();
+            v[u] = i < end && key[i] < V ? P::load(dout + sidx[i] * a.ld_dout) : P::zero();
         }
+    };
+    auto add = [&](const P(&v)[kGradUnroll], unsigned i0) {
 #pragma unroll
         for (int u = 0; u < kGradUnroll; ++u) {
-            if (i0 + u < end && k[u] != cur) {
+            if (i0 + u < end && key[i0 + u] != cur) {
                 if (began) {
                     finish<TO, N>(a, cur, col, s);
                 } else {
                     store_part<N>(part, s);
                 }
                 began = true;
-                cur = k[u];
+                cur = key[i0 + u];
 #pragma unroll
                 for (int e = 0; e < N; ++e) s[e] = 0.f;
             }
@@ -270,9 +325,17 @@ __global__ void __launch_bounds__(256) embed_grad_kernel(const EmbedArgs a) {
 #pragma unroll
             for (int e = 0; e < N; ++e) s[e] += f[e];
         }
+    };
+    P v[kGradUnroll], w[kGradUnroll];
+    load(v, begin);
+    for (unsigned i0 = begin; i0 < end; i0 += 2 * kGradUnroll) {
+        load(w, i0 + kGradUnroll);
+        add(v, i0);
+        load(v, i0 + 2 * kGradUnroll);
+        add(w, i0 + kGradUnroll);
     }
     if (cur >= V) return;  // ids outside the table come last
-    const bool more = end < n && key[end] == cur;
+    const bool more = key[end] == cur;
     if (began && !more) {
         finish<TO, N>(a, cur, col, s);
     } else {
@@ -282,57 +345,77 @@ __global__ void __launch_bounds__(256) embed_grad_kernel(const EmbedArgs a) {
 }
 
 // The ids that span pieces: for each listed piece p, its partial row 1 plus the rows 0 of the
-// pieces that follow while the id goes on. Block: 32 x 4 columns, 8 slices of the pieces.
+// pieces that follow while the id goes on, always in the same grouping. A warp takes one of them
+// for 32 x 4 columns; those of more than kJoinShort rows are shared by the block's eight warps.
+constexpr unsigned kJoinShort = 16;
+
+template <typename TO>
+__device__ __forceinline__ void finish_columns(const EmbedArgs &a, uint32_t id, int col, float4 s) {
+    const float f[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float one[1] = {f[e]};
+        if (col + e < a.D) finish<TO, 1>(a, id, col + e, one);
+    }
+}
+
 template <typename TO>
 __global__ void __launch_bounds__(256) embed_join_kernel(const EmbedArgs a) {
     __shared__ float4 sums[8][32];
+    __shared__ unsigned long_piece[8], long_rows[8];
     pdl_wait();
     const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int col = (blockIdx.y * 32 + lane) * 4;
+    const unsigned S = a.S, npieces = a.npieces;
     const uint32_t count = *a.count;
-    for (uint32_t i = blockIdx.x; i < count; i += gridDim.x) {
-        const unsigned p = a.list[i];
-        const uint32_t id = a.key[0][p * static_cast<unsigned>(a.S)  + a.S - 1];
-        // the pieces p + 1 .. p + m hold the rest: piece q has some of it when its first is id
-        unsigned m = 0;
-        for (;;) {
-            const unsigned q = p + 1 + m + lane;
-            const bool has = q < static_cast<unsigned>(a.npieces) &&
-                             a.key[0][q * static_cast<unsigned>(a.S)] == id;
-            const uint32_t not_in = ~__ballot_sync(0xffffffffu, has);
-            if (not_in) {
-                m += __ffs(not_in) - 1;
-                break;
-            }
-            m += 32;
-        }
+    // rows j0 .. j1 - 1 of piece p's id: row 0 is its partial row 1, row j piece (p + j)'s row 0
+    auto rows_sum = [&](unsigned p, unsigned j0, unsigned j1) {
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         if (col < a.Dp) {
-            // rows 0 .. m: row 0 is piece p's partial row 1, row j > 0 piece (p + j)'s row 0
-            const unsigned per = (m + 8) / 8, j1 = min((y + 1) * per, m + 1);
-#pragma unroll 4
-            for (unsigned j = y * per; j < j1; ++j) {
+#pragma unroll 8
+            for (unsigned j = j0; j < j1; ++j) {
                 const float4 v = *reinterpret_cast<const float4 *>(
                     a.part + (static_cast<size_t>(p + j) * 2 + (j == 0)) * a.Dp + col);
                 s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
             }
         }
-        sums[y][lane] = s;
-        __syncthreads();
-        if (y == 0) {
-#pragma unroll
-            for (int w = 1; w < 8; ++w) {
-                const float4 v = sums[w][lane];
-                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        return s;
+    };
+    for (uint32_t i0 = blockIdx.x * 8; i0 < count; i0 += gridDim.x * 8) {
+        unsigned p = 0, rows = 0;
+        if (i0 + y < count) {
+            p = a.list[i0 + y];
+            const uint32_t id = a.key[0][(p + 1) * S - 1];
+            for (;;) {  // piece q has some of it when its first token has the id
+                const unsigned q = p + 1 + rows + lane;
+                const bool has = q < npieces && a.key[0][q * S] == id;
+                const uint32_t not_in = ~__ballot_sync(0xffffffffu, has);
+                rows += not_in ? __ffs(not_in) - 1 : 32;
+                if (not_in) break;
             }
-            const float f[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float one[1] = {f[e]};
-                if (col + e < a.D) finish<TO, 1>(a, id, col + e, one);
-            }
+            ++rows;  // and its own
+            if (rows <= kJoinShort) finish_columns<TO>(a, id, col, rows_sum(p, 0, rows));
         }
+        if (lane == 0) long_piece[y] = p, long_rows[y] = rows > kJoinShort ? rows : 0;
         __syncthreads();
+        for (int k = 0; k < 8; ++k) {
+            const unsigned m = long_rows[k], q = long_piece[k];
+            if (!m) continue;  // the same for the whole block
+            const unsigned per = (m + 7) / 8;
+            sums[y][lane] = rows_sum(q, min(y * per, m), min((y + 1) * per, m));
+            __syncthreads();
+            if (y == 0) {
+                float4 s = sums[0][lane];
+#pragma unroll
+                for (int w = 1; w < 8; ++w) {
+                    const float4 v = sums[w][lane];
+                    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+                }
+                finish_columns<TO>(a, a.key[0][(q + 1) * S - 1], col, s);
+            }
+            __syncthreads();
+        }
+        __syncthreads();  // the long ones' lists may be written again
     }
 }
 
@@ -348,8 +431,9 @@ size_t sort_smem(int bits) { return (size_t(kSortWarps) + 2) * (size_t(4) << bit
 
 template <typename T, typename TO, int N>
 cudaError_t launch_grad(const EmbedArgs &a, cudaStream_t st) {
-    const int units = a.D / N;
-    const int tx = units < 256 ? units : 256, ty = 256 / tx;
+    // as many pieces per block as its 256 threads and its stretch of 256 tokens hold
+    const int units = a.D / N, tx = units < 256 ? units : 256, fit = 256 / tx, room = 256 / a.S;
+    const int ty = fit < room ? fit : room;
     return launch_pdl(embed_grad_kernel<T, TO, N>,
                       dim3((a.npieces + ty - 1) / ty, (units + tx - 1) / tx), dim3(tx, ty), 0, st, a);
 }
@@ -375,16 +459,31 @@ void embed_sort_plan(EmbedArgs &a) {
     a.bits = (bits + a.passes - 1) / a.passes;
 }
 
-cudaError_t launch_embed_sort(const EmbedArgs &a, int bf16_out, int vec, int num_sms,
-                              cudaStream_t st) {
-    const int clusters = a.accumulate ? 1 : num_sms / kSortCluster;
-    const dim3 grid((clusters > 2 ? clusters : a.accumulate ? 1 : 2) * kSortCluster);
-    const size_t smem = sort_smem(a.bits);
+// One CTA while its warps hold their tokens in registers; then up to eight, which share them. The
+// zeros take the other SMs, or with clusters seven eighths of all (so that every cluster finds
+// its place at once).
+cudaError_t launch_embed_sort(EmbedArgs a, int bf16_out, int vec, int num_sms, cudaStream_t st) {
+    a.sort_ctas = 1;
+    while (a.sort_ctas < 8 && a.n > a.sort_ctas * kSortThreads * kSortKeep) a.sort_ctas *= 2;
+    const int all = a.sort_ctas == 1 ? num_sms : num_sms * 7 / 8 / a.sort_ctas * a.sort_ctas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.accumulate ? a.sort_ctas : all < 2 * a.sort_ctas ? 2 * a.sort_ctas : all);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = sort_smem(a.bits);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.sort_ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.sort_ctas > 1 ? 2 : 1;
     if (bf16_out)
-        return vec ? launch_pdl(embed_sort_kernel<__nv_bfloat16, 8>, grid, dim3(kSortThreads), smem, st, a)
-                   : launch_pdl(embed_sort_kernel<__nv_bfloat16, 1>, grid, dim3(kSortThreads), smem, st, a);
-    return vec ? launch_pdl(embed_sort_kernel<float, 4>, grid, dim3(kSortThreads), smem, st, a)
-               : launch_pdl(embed_sort_kernel<float, 1>, grid, dim3(kSortThreads), smem, st, a);
+        return vec ? cudaLaunchKernelEx(&cfg, embed_sort_kernel<__nv_bfloat16, 8>, a)
+                   : cudaLaunchKernelEx(&cfg, embed_sort_kernel<__nv_bfloat16, 1>, a);
+    return vec ? cudaLaunchKernelEx(&cfg, embed_sort_kernel<float, 4>, a)
+               : cudaLaunchKernelEx(&cfg, embed_sort_kernel<float, 1>, a);
 }
 
 cudaError_t launch_embed_grad(const EmbedArgs &a, int bf16, int bf16_out, int vec, cudaStream_t st) {
@@ -394,22 +493,10 @@ cudaError_t launch_embed_grad(const EmbedArgs &a, int bf16, int bf16_out, int ve
 }
 
 cudaError_t launch_embed_join(const EmbedArgs &a, int bf16_out, int num_sms, cudaStream_t st) {
-    const dim3 grid(a.npieces < 2 * num_sms ? a.npieces : 2 * num_sms, (a.Dp / 4 + 31) / 32);
+    const int gx = (a.npieces + 7) / 8, most = 2 * num_sms;
+    const dim3 grid(gx < most ? gx : most, (a.Dp / 4 + 31) / 32);
     return bf16_out ? launch_pdl(embed_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, a)
                     : launch_pdl(embed_join_kernel<float>, grid, dim3(256), 0, st, a);
-}
-
-cudaError_t embed_kernels_configure() {
-    const int smem = static_cast<int>(sort_smem(kSortMaxBits));
-    const void *kernels[] = {reinterpret_cast<const void *>(embed_sort_kernel<__nv_bfloat16, 8>),
-                             reinterpret_cast<const void *>(embed_sort_kernel<__nv_bfloat16, 1>),
-                             reinterpret_cast<const void *>(embed_sort_kernel<float, 4>),
-                             reinterpret_cast<const void *>(embed_sort_kernel<float, 1>)};
-    for (const void *k : kernels) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
 }
 
 }  // namespace rsa

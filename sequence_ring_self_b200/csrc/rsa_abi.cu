@@ -282,7 +282,6 @@ rsa_status_t device_state(DeviceState **out) {
             (e = rsa::fwd_kernels_configure()) != cudaSuccess ||
             (e = rsa::linear_kernels_configure()) != cudaSuccess ||
             (e = rsa::qk_kernels_configure()) != cudaSuccess ||
-            (e = rsa::embed_kernels_configure()) != cudaSuccess ||
             (e = rsa::distill_kernels_configure()) != cudaSuccess)
             return cuda_fail("cudaFuncSetAttribute", e);
         void *ptr = nullptr;
@@ -1139,9 +1138,10 @@ struct EmbedLayout {
 
 EmbedLayout embed_layout(int n, int D) {
     EmbedLayout y{};
-    // pieces of 8 to 256 tokens, about 512 of them
-    const int s = (n / 512 + 7) / 8 * 8;
-    y.S = s < 8 ? 8 : s > 256 ? 256 : s;
+    // pieces of 8 to 256 tokens, so many that their 16-byte columns (of bf16) make about as many
+    // threads as the GPU runs at a time
+    const long long s = static_cast<long long>(n) * ((D + 7) / 8) / (kSms * 512) / 8 * 8;
+    y.S = s < 8 ? 8 : s > 256 ? 256 : static_cast<int>(s);
     y.npieces = n / y.S + (n % y.S != 0);
     y.Dp = (D + 3) / 4 * 4;
     y.key_bytes = align_up(size_t(n) * 4, kAlign);

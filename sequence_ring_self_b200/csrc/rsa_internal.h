@@ -169,16 +169,16 @@ struct EmbedArgs {
     uint32_t *count, *list;          // pieces whose last id goes on behind them
     float *part;                     // [npieces][2][Dp] partial rows
     int S, npieces, Dp;
+    int sort_ctas;                   // set by the launch
 };
 // vec: rows and columns allow 16-byte accesses.
 cudaError_t launch_embed(const EmbedArgs &a, int bf16, int vec, cudaStream_t st);
 void embed_sort_plan(EmbedArgs &a);  // sets a.passes and a.bits for a.V
-// Sort, sums, joins; bf16_out: the table's gradient is bf16 (fp32 otherwise).
-cudaError_t launch_embed_sort(const EmbedArgs &a, int bf16_out, int vec, int num_sms,
-                              cudaStream_t st);
+// Sort (and zeros, unless a.accumulate), sums, joins; bf16_out: the table's gradient is bf16 (fp32
+// otherwise).
+cudaError_t launch_embed_sort(EmbedArgs a, int bf16_out, int vec, int num_sms, cudaStream_t st);
 cudaError_t launch_embed_grad(const EmbedArgs &a, int bf16, int bf16_out, int vec, cudaStream_t st);
 cudaError_t launch_embed_join(const EmbedArgs &a, int bf16_out, int num_sms, cudaStream_t st);
-cudaError_t embed_kernels_configure();
 
 struct DistillArgs {
     const void *z, *index, *teacher;
