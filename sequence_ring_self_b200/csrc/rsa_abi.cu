@@ -1138,8 +1138,9 @@ struct EmbedLayout {
 
 EmbedLayout embed_layout(int n, int D) {
     EmbedLayout y{};
-    // pieces of 8 to 256 tokens, so many that their 16-byte columns (of bf16) make about as many
-    // threads as the GPU runs at a time
+    // pieces of 8 to 256 tokens, so many that their 16-byte columns (of bf16) make about 512
+    // threads per SM: twice as many leave more ids to join (32768 tokens, 60000 x 512: 58 us
+    // instead of 51), and gain nothing elsewhere
     const long long s = static_cast<long long>(n) * ((D + 7) / 8) / (kSms * 512) / 8 * 8;
     y.S = s < 8 ? 8 : s > 256 ? 256 : static_cast<int>(s);
     y.npieces = n / y.S + (n % y.S != 0);
