@@ -128,7 +128,7 @@ RSA_API rsa_status_t rsa_embed_backward(const void *ids, int ids64, const void *
  * logits [n, V], rows ld elements apart, type dt; index [n, K] int64 (index64 != 0) or int32;
  * teacher [n, K] of type teacher_dt; loss fp32 [n]; stats fp32 [n, 2] (8-byte aligned). Logits
  * need no alignment beyond the element's. 1 <= V < 2^31 - 1, 1 <= K <= RSA_DISTILL_MAX_K,
- * temperature > 0, 0 <= n < 2^27 (0 launches nothing).
+ * 1e-18 <= temperature <= 1e18, 0 <= n < 2^27 (0 launches nothing).
  */
 #define RSA_DISTILL_MAX_K 1024
 

@@ -1157,7 +1157,8 @@ rsa_status_t distill_args(rsa::DistillArgs &a, const void *logits, long long ld,
                           const void *index, int index64, const void *teacher,
                           rsa_dtype_t teacher_dt, int n, int V, int K, float temperature,
                           rsa_dtype_t dt) {
-    if (n < 0 || V <= 0 || K <= 0 || !(temperature > 0.f) || isinf(temperature))
+    // (1 / temperature and its square stay finite in fp32 with room to spare)
+    if (n < 0 || V <= 0 || K <= 0 || !(temperature >= 1e-18f) || !(temperature <= 1e18f))
         return RSA_ERR_INVALID_ARG;
     if (!dtype_ok(dt) || !dtype_ok(teacher_dt) || K > RSA_DISTILL_MAX_K || V == 0x7fffffff ||
         n >= (1 << 27))

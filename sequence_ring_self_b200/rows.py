@@ -24,6 +24,7 @@ captured graphs) need one each. The functions can be captured into a CUDA graph;
 from __future__ import annotations
 
 import ctypes
+from functools import lru_cache
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -85,6 +86,16 @@ def _given_workspace(workspace, device):
     return workspace
 
 
+@lru_cache(maxsize=None)
+def _qk_workspace(d):
+    return int(rsa.load_library().rsa_qk_norm_rope_workspace_size(d))
+
+
+@lru_cache(maxsize=256)
+def _embed_workspace(n, V, D):
+    return int(rsa.load_library().rsa_embed_workspace_size(n, V, D))
+
+
 def _nbytes(t):
     return t.numel() * t.element_size()
 
@@ -113,8 +124,7 @@ def _like(t):
 
 def _qk_checked(q, k, wq, wk, freq, positions, *same):
     """Checks what both passes share; `same` are the tensors shaped like q and k in turn, or None.
-    Returns the device, the arguments from the frequencies to the type, and the tensors' strides
-    (those of outputs still to be allocated excepted)."""
+    Returns the device and, as the C call has them, the positions, the sizes and the type."""
     dt = _dtype(q)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("queries and keys must be [B, heads, L, d]")
@@ -126,10 +136,12 @@ def _qk_checked(q, k, wq, wk, freq, positions, *same):
         raise ValueError("queries and keys must agree in B, L and d")
     _int32(B, Hq, ks[1], L, d)
     device = _on_gpu(q, k, wq, wk, freq, positions, *same)
-    for i, t in enumerate((q, k) + same):
+    if d > 1 and (q.stride(3) != 1 or k.stride(3) != 1):
+        raise ValueError("rows of d elements must be contiguous")
+    for i, t in enumerate(same):
         if t is None:
             continue
-        if i > 1:
+        if t.shape != (ks if i & 1 else qs) or t.dtype != q.dtype:
             _shaped("a tensor like the " + ("keys" if i & 1 else "queries"), t, ks if i & 1 else qs, q.dtype)
         if t.stride(3) != 1 and d > 1:
             raise ValueError("rows of d elements must be contiguous")
@@ -173,8 +185,8 @@ def qk_norm_rope(q, k, wq, wk, freq, *, pos0: int = 0, positions=None, eps: floa
         ok = _like(k) if out_k is None else out_k
         st = _S12(*q.stride()[:3], *k.stride()[:3], *oq.stride()[:3], *ok.stride()[:3])
         rc = lib.rsa_qk_norm_rope(q.data_ptr(), k.data_ptr(), oq.data_ptr(), ok.data_ptr(), st,
-                                  _addr(wq), _addr(wk), *pos, pos0, *sizes, bool(interleaved),
-                                  eps, dt, s)
+                                  _addr(wq), _addr(wk), *pos, int(pos0), *sizes,
+                                  bool(interleaved), float(eps), dt, s)
         return rc, (oq, ok)
 
     return _call("rsa_qk_norm_rope", device, stream, (q, k, wq, wk, freq, positions, out_q, out_k),
@@ -197,8 +209,7 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, wq, wk, freq, *, pos0: int = 0, 
         gk = _like(k) if dk is None else dk
         dwq = dwk = ws = None
         if need_weights and (wq is not None or wk is not None):
-            ws = (torch.empty(max(lib.rsa_qk_norm_rope_workspace_size(d), 256), dtype=torch.uint8,
-                              device=device)
+            ws = (torch.empty(max(_qk_workspace(d), 256), dtype=torch.uint8, device=device)
                   if workspace is None else _given_workspace(workspace, device))
             dwq = None if wq is None else torch.empty_like(wq)
             dwk = None if wk is None else torch.empty_like(wk)
@@ -206,8 +217,8 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, wq, wk, freq, *, pos0: int = 0, 
                   *gq.stride()[:3], *gk.stride()[:3])
         rc = lib.rsa_qk_norm_rope_backward(
             q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), gq.data_ptr(),
-            gk.data_ptr(), st, _addr(wq), _addr(wk), _addr(dwq), _addr(dwk), *pos, pos0, *sizes,
-            bool(interleaved), eps, dt, _addr(ws), 0 if ws is None else _nbytes(ws), s)
+            gk.data_ptr(), st, _addr(wq), _addr(wk), _addr(dwq), _addr(dwk), *pos, int(pos0),
+            *sizes, bool(interleaved), float(eps), dt, _addr(ws), 0 if ws is None else _nbytes(ws), s)
         return rc, (gq, gk, dwq, dwk)
 
     return _call("rsa_qk_norm_rope_backward", device, stream,
@@ -216,10 +227,10 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, wq, wk, freq, *, pos0: int = 0, 
 
 def qk_norm_rope_workspace_size(d: int) -> int:
     """Workspace bytes of ``qk_norm_rope_backward``."""
-    n = rsa.load_library().rsa_qk_norm_rope_workspace_size(int(d))
+    n = _qk_workspace(int(d))
     if n == 0:
         raise rsa.RSAError(rsa.RSA_ERR_UNSUPPORTED, "rsa_qk_norm_rope_workspace_size")
-    return int(n)
+    return n
 
 
 def _vector_rows(t):
@@ -302,7 +313,7 @@ def embed(ids, table, scale: float = 1.0, *, out=None, stream: torch.cuda.Stream
         o = table.new_empty(shape) if out is None else out
         ldo = D if out is None else _ld(_flat("out", o, D))
         rc = lib.rsa_embed(ids.data_ptr(), i64, table.data_ptr(), ld, o.data_ptr(), ldo, n, V, D,
-                           scale, dt, s)
+                           float(scale), dt, s)
         return rc, o
 
     return _call("rsa_embed", device, stream, (ids, table, out), body)
@@ -331,11 +342,10 @@ def embed_backward(ids, dout, num_rows: int, scale: float = 1.0, *, dtable=None,
 
     def body(lib, s):
         dtab = dout.new_empty((V, D)) if dtable is None else dtable
-        ws = (torch.empty(max(lib.rsa_embed_workspace_size(n, V, D), 256), dtype=torch.uint8,
-                          device=device)
+        ws = (torch.empty(max(_embed_workspace(n, V, D), 256), dtype=torch.uint8, device=device)
               if workspace is None else _given_workspace(workspace, device))
         rc = lib.rsa_embed_backward(ids.data_ptr(), i64, g.data_ptr(), ld, dtab.data_ptr(),
-                                    D if dtable is None else _ld(dtab), n, V, D, scale,
+                                    D if dtable is None else _ld(dtab), n, V, D, float(scale),
                                     bool(accumulate), dt, _DT[dtab.dtype], ws.data_ptr(),
                                     _nbytes(ws), s)
         return rc, dtab
@@ -346,7 +356,7 @@ def embed_backward(ids, dout, num_rows: int, scale: float = 1.0, *, dtable=None,
 def embed_workspace_size(n: int, num_rows: int, D: int) -> int:
     """Workspace bytes of ``embed_backward`` for n tokens (0: none needed)."""
     _int32(int(n), int(num_rows), int(D))
-    return int(rsa.load_library().rsa_embed_workspace_size(int(n), int(num_rows), int(D)))
+    return _embed_workspace(int(n), int(num_rows), int(D))
 
 
 class Embedding(torch.autograd.Function):
@@ -385,7 +395,7 @@ def _distill_checked(logits, index, teacher, temperature, *more):
     n = z.shape[0]
     _int32(n, V, K)
     head = (z.data_ptr(), _ld(z), index.data_ptr(), i64, teacher.data_ptr(), tdt)
-    return device, shape[:-1], head, (n, V, K, temperature, dt)
+    return device, shape[:-1], head, (n, V, K, float(temperature), dt)
 
 
 def _rows_of(name, t, shape):

@@ -630,6 +630,60 @@ def test_given_workspaces():
         rows.embed_backward(ids, dout, 70, workspace=ws[:-512])
 
 
+def test_offsets_past_32_bits():
+    """Rows more than 2^31 elements into a tensor: the last ones of 4.3 GB of queries, table, gradient
+    and logits, against the same rows by themselves."""
+    far = (1 << 31) + 4096
+    buf = torch.empty(far + 4096, dtype=BF16, device="cuda")
+    x, k, dy = randn(gen(70), 2, 1, 5, 64, dt=BF16), randn(gen(71), 2, 1, 5, 64, dt=BF16), randn(gen(72), 2, 1, 5, 64, dt=BF16)
+    w, freq = torch.ones(64, device="cuda"), torch.rand(32, generator=gen(73)).cuda()
+    q = buf.as_strided((2, 1, 5, 64), (far, 320, 64, 1))
+    q.copy_(x)
+    assert same(rows.qk_norm_rope(q, k, w, w, freq)[0], rows.qk_norm_rope(x, k, w, w, freq)[0])
+    ref = rows.qk_norm_rope_backward(x, k, dy, dy, w, w, freq)
+    got = rows.qk_norm_rope_backward(q, k, dy, dy, w, w, freq, dq=q)
+    assert all(same(a, b) for a, b in zip(got, ref))
+    # a table and its gradient: 2^25 + 64 rows of 64
+    V = far // 64 + 60
+    table = buf[:V * 64].view(V, 64)
+    ids = torch.tensor([V - 1, 3, V - 2, V - 1], device="cuda")
+    table[ids] = x.view(10, 64)[:4]
+    assert same(rows.embed(ids, table, 2.0), rows.embed(torch.arange(4, device="cuda"), table[ids].clone(), 2.0))
+    rows.embed_backward(ids, dy.view(10, 64)[:4], V, dtable=table)
+    small = rows.embed_backward(torch.tensor([2, 0, 1, 2], device="cuda"), dy.view(10, 64)[:4], 3)
+    assert same(table[[V - 1, 3, V - 2]], small[[2, 0, 1]]) and (table[V - 3] == 0).all() and (table[:3] == 0).all()
+    # logits: the last of 65536 rows of 32768, the others without a slot
+    V = 32768
+    n = buf.numel() // V
+    z = buf[:n * V].view(n, V)
+    zs, index, teacher, dloss = distill_case(74, 3, V, 9, BF16, pad=False)
+    z[n - 3:] = zs
+    many = torch.full((n, 9), -1, device="cuda")
+    many[n - 3:] = index
+    t = torch.zeros(n, 9, device="cuda")
+    t[n - 3:] = teacher
+    d = torch.zeros(n, device="cuda")
+    d[n - 3:] = dloss
+    loss, stats = rows.distill(z, many, t)
+    ref, bound, _, _ = ro.distill(zs, index, teacher, 1.0)
+    ro.check(loss[n - 3:], ref, bound, "loss")
+    rows.distill_step(z, many, t, d, dlogits=z)
+    dref, dbound = ro.distill_backward(zs, index, teacher, dloss, 1.0)
+    ro.check(z[n - 3:], dref, dbound, "dlogits")
+    assert (z[:n - 3] == 0).all()
+
+
+def test_numbers_of_other_types():
+    """numpy's numbers, where a Python number is meant."""
+    import numpy as np
+
+    q, k, w, freq, _, _ = qk_case(75, 1, 1, 1, 5, 64, F32)
+    assert same(rows.qk_norm_rope(q, k, *w, freq, pos0=np.int64(3), eps=np.float32(1e-5))[0],
+                rows.qk_norm_rope(q, k, *w, freq, pos0=3, eps=float(np.float32(1e-5)))[0])
+    z, index, teacher, _ = distill_case(76, 3, 50, 2, F32)
+    assert same(rows.distill(z, index, teacher, np.float32(2))[0], rows.distill(z, index, teacher, 2)[0])
+
+
 def test_a_training_step_of_the_operators_together():
     """tokens -> embed -> projection -> norm and rotation -> ring attention -> projection ->
     distillation, forward and backward in fp32 through the autograd wrappers, against the same

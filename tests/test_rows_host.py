@@ -120,7 +120,7 @@ def dist(lib, kind, z=far(0), ld=100, index=far(1), teacher=far(2), tdt=rsa.RSA_
 def test_distill_refusals(lib, kind):
     call = lambda **kw: dist(lib, kind, **kw)
     for bad in (dict(n=-1), dict(V=0), dict(K=0), dict(tau=0.0), dict(tau=-1.0), dict(tau=math.nan),
-                dict(tau=math.inf), dict(z=0), dict(z=far(0) + 1), dict(index=0), dict(index=far(1) + 4),
+                dict(tau=math.inf), dict(tau=1e-19), dict(tau=1e19), dict(z=0), dict(z=far(0) + 1), dict(index=0), dict(index=far(1) + 4),
                 dict(teacher=0), dict(teacher=far(2) + 2), dict(ld=-1)):
         assert call(**bad) == INVALID, bad
     for bad in (dict(K=1025), dict(V=0x7fffffff), dict(n=1 << 27), dict(dt=9), dict(tdt=9)):
