@@ -565,10 +565,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
 // gradient first (from L2, in practice).
 // Threads resident per SM: 768 in CTAs of up to 256, or one CTA of kStepWide for rows that need the
 // whole SM's memory (more threads would not get the registers: 640 threads 504 us, 768 534, 1024
-// 646 instead of 490 for 4096 rows of 131072 bf16 logits; three CTAs of 256 read most of the row a
+// 646 where 512 took 490, for 4096 rows of 131072 bf16 logits; three CTAs of 256 read most of the row a
 // second time from HBM, since 444 such rows do not stay in L2: 614). Vectors of a batch, and how many
 // batches later it is added.
-constexpr int kStepWide = 512;
+constexpr int kStepWide = 512, kStepAhead = 256 * 1024;
 constexpr int step_threads(int nt) { return nt == kStepWide ? nt : 768; }
 constexpr int step_batch(int nt) { return nt == kStepWide ? 4 : 2; }
 constexpr int step_lag(int nt) { return nt == kStepWide ? 2 : 3; }
@@ -648,6 +648,14 @@ __global__ void __launch_bounds__(NT, step_threads(NT) / NT) distill_step_kernel
             rows.walk(cur, ring, nb, [&](int, P(&v)[U]) { rows.add(r, v); });
         }
 
+        if (has_next && tid == 0) {
+            // the next row on its way to L2 while this one is brought to its end (sent for at the
+            // start of the row it pushes out what is still to be read: 571 us instead of 469)
+            const typename R::Share next = rows.share_of(next_row);
+            const int bytes = min(next.n * 16, kStepAhead);
+            if (bytes)
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(next.zv), "r"(bytes) : "memory");
+        }
         // the next row's slots and their logits, read before anything of that row is replaced
         const int next_place = (place + 1) % kPlaces, old_place = (place + kPlaces - 1) % kPlaces;
         bool live = false;
@@ -693,13 +701,16 @@ __global__ void __launch_bounds__(NT, step_threads(NT) / NT) distill_step_kernel
 size_t lists_bytes(int K) { return size_t(kPlaces) * 3 * 4 * ((K + 3) & ~3); }
 
 template <typename Kernel>
-cudaError_t launch_rows(Kernel kernel, const DistillArgs &a, int nt, int threads, size_t smem,
+cudaError_t launch_rows(Kernel kernel, const DistillArgs &a, int nt, int threads, bool even, size_t smem,
                         int num_sms, cudaStream_t st) {
     int per_sm = threads / nt;
     const int by_smem = static_cast<int>(size_t(226) * 1024 / (smem + 2048));
     if (by_smem < per_sm) per_sm = by_smem < 1 ? 1 : by_smem;
-    int rows = (per_sm * num_sms) >> a.log_cluster;  // at a time
+    // at a time; `even`: as many as leave every CTA the same number of them (the loss of 4096 rows:
+    // 52 us instead of 55; loss and gradient in one pass lose by it, 132 instead of 125)
+    int rows = (per_sm * num_sms) >> a.log_cluster;
     if (rows > a.n) rows = a.n;
+    if (even) rows = (a.n + (a.n + rows - 1) / rows - 1) / ((a.n + rows - 1) / rows);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows) << a.log_cluster);
     cfg.blockDim = dim3(nt);
@@ -719,9 +730,10 @@ cudaError_t launch_rows(Kernel kernel, const DistillArgs &a, int nt, int threads
 // Shared memory for a.ring batches of loss and gradient in one pass: an even share of an SM's.
 constexpr int kStepSmem = 200 * 1024, kSmemMost = 224 * 1024;  // (227 KB less the static part)
 
-// Threads per SM of a pass over the rows. Many long rows: half of what fits, which leaves DRAM
-// longer runs (the gradient of 4096 rows of 32768 bf16 logits: 102 us instead of 109).
-int pass_threads(const DistillArgs &a, int size, int num_sms) {
+// Threads per SM of the gradient's pass. Many long rows: half of what fits, which leaves DRAM longer
+// runs (4096 rows of 32768 bf16 logits: 101 us instead of 110; the loss alone takes 59 instead of
+// 52 that way).
+int gradient_threads(const DistillArgs &a, int size, int num_sms) {
     return a.n >= 16 * num_sms && static_cast<long long>(a.V) * size >= 32768 ? 512 : 1024;
 }
 
@@ -734,10 +746,11 @@ cudaError_t launch(DistillArgs a, int num_sms, cudaStream_t st) {
         const int share = kStepSmem / (step_threads(NT) / NT), left = kSmemMost - static_cast<int>(lists_bytes(a.K));
         const int nb = (per * 16 + batch - 1) / batch, most = (share < left ? share : left) / batch;
         a.ring = nb < 1 ? 1 : nb < most ? nb : most;
-        return launch_rows(distill_step_kernel<T, NT>, a, NT, step_threads(NT), size_t(a.ring) * batch + lists_bytes(a.K),
+        return launch_rows(distill_step_kernel<T, NT>, a, NT, step_threads(NT), false, size_t(a.ring) * batch + lists_bytes(a.K),
                            num_sms, st);
     } else {
-        return launch_rows(distill_kernel<T, MODE == kBackward, NT>, a, NT, pass_threads(a, static_cast<int>(sizeof(T)), num_sms),
+        return launch_rows(distill_kernel<T, MODE == kBackward, NT>, a, NT,
+                           MODE == kBackward ? gradient_threads(a, static_cast<int>(sizeof(T)), num_sms) : 1024, true,
                            size_t(kRing) * batch + lists_bytes(a.K), num_sms, st);
     }
 }

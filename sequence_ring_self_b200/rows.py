@@ -146,10 +146,9 @@ def _qk_checked(q, k, wq, wk, freq, positions, *same):
         if t.stride(3) != 1 and d > 1:
             raise ValueError("rows of d elements must be contiguous")
     for w in (wq, wk):
-        if w is not None:
+        if w is not None and (w.dtype != torch.float32 or w.shape != (d,) or not w.is_contiguous()):
             _shaped("a norm's weight", w, (d,), torch.float32)
-            if not w.is_contiguous():
-                raise ValueError("a norm's weight must be contiguous")
+            raise ValueError("a norm's weight must be contiguous")
     rot = 0
     if freq is not None:
         if freq.dtype != torch.float32 or freq.dim() != 1 or not freq.is_contiguous():
@@ -183,7 +182,7 @@ def qk_norm_rope(q, k, wq, wk, freq, *, pos0: int = 0, positions=None, eps: floa
     def body(lib, s):
         oq = _like(q) if out_q is None else out_q
         ok = _like(k) if out_k is None else out_k
-        st = _S12(*q.stride()[:3], *k.stride()[:3], *oq.stride()[:3], *ok.stride()[:3])
+        st = _S12(*(q.stride()[:3] + k.stride()[:3] + oq.stride()[:3] + ok.stride()[:3]))
         rc = lib.rsa_qk_norm_rope(q.data_ptr(), k.data_ptr(), oq.data_ptr(), ok.data_ptr(), st,
                                   _addr(wq), _addr(wk), *pos, int(pos0), *sizes,
                                   bool(interleaved), float(eps), dt, s)
@@ -213,8 +212,8 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, wq, wk, freq, *, pos0: int = 0, 
                   if workspace is None else _given_workspace(workspace, device))
             dwq = None if wq is None else torch.empty_like(wq)
             dwk = None if wk is None else torch.empty_like(wk)
-        st = _S18(*q.stride()[:3], *k.stride()[:3], *dq_out.stride()[:3], *dk_out.stride()[:3],
-                  *gq.stride()[:3], *gk.stride()[:3])
+        st = _S18(*(q.stride()[:3] + k.stride()[:3] + dq_out.stride()[:3] + dk_out.stride()[:3]
+                    + gq.stride()[:3] + gk.stride()[:3]))
         rc = lib.rsa_qk_norm_rope_backward(
             q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), gq.data_ptr(),
             gk.data_ptr(), st, _addr(wq), _addr(wk), _addr(dwq), _addr(dwk), *pos, int(pos0),
