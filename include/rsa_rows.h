@@ -86,7 +86,8 @@ RSA_API rsa_status_t rsa_qk_norm_rope_backward(const void *Q, const void *K, con
  * zeros (padding, or another rank's part of the vocabulary).
  * ids: int64 (ids64 != 0) or int32 [n]; table [V, D] and out [n, D] of type dt, rows ld_table
  * and ld_out elements apart; no alignment beyond the element's is needed (rows on 16-byte
- * boundaries are faster). n, D >= 0 (zero launches nothing), 1 <= V < 2^31 - 1.
+ * boundaries are faster). n, D >= 0 (zero launches nothing), 1 <= V < 2^31 - 1, D <= 2^20,
+ * n * D < 2^40.
  */
 RSA_API rsa_status_t rsa_embed(const void *ids, int ids64, const void *table, long long ld_table,
                                void *out, long long ld_out, int n, int V, int D, float scale,

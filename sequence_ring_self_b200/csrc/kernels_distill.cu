@@ -480,9 +480,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
         }
         alive = __syncthreads_or(live);
         if (!alive) cp_async_wait<0>();
-        if (BACKWARD) {
-            rows.finish_slots(0, join_warps(red_slots[1], c), 0.f, 0.f);
-        }
+        if (BACKWARD) rows.finish_slots(0, join_warps(red_slots[1], c), 0.f, 0.f);
     }
 
     for (; row < a.n; row += stride, par ^= 1) {
@@ -652,7 +650,7 @@ __global__ void __launch_bounds__(NT, step_threads(NT) / NT) distill_step_kernel
             // the next row on its way to L2 while this one is brought to its end (sent for at the
             // start of the row it pushes out what is still to be read: 571 us instead of 469)
             const typename R::Share next = rows.share_of(next_row);
-            const int bytes = min(next.n * 16, kStepAhead);
+            const int bytes = min(next.n, kStepAhead / 16) * 16;
             if (bytes)
                 asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(next.zv), "r"(bytes) : "memory");
         }
@@ -685,9 +683,7 @@ __global__ void __launch_bounds__(NT, step_threads(NT) / NT) distill_step_kernel
             float m;
             const float logsum = log_of(q, m);
             const float l = warp_sum(rows.finish_slots(place, t, m, logsum));
-            if (lane == 0) {
-                red_loss[par][warp] = alive ? l : 0.f;
-            }
+            if (lane == 0) red_loss[par][warp] = alive ? l : 0.f;
             if (tid == 0) row_stats[par] = make_float2(m, logsum);
         }
         __syncthreads();  // the statistics
@@ -743,11 +739,13 @@ cudaError_t launch(DistillArgs a, int num_sms, cudaStream_t st) {
     if constexpr (MODE == kStep) {
         const int nv = a.V / (16 / static_cast<int>(sizeof(T)));
         const int per = (nv + (1 << a.log_cluster) - 1) >> a.log_cluster;
-        const int share = kStepSmem / (step_threads(NT) / NT), left = kSmemMost - static_cast<int>(lists_bytes(a.K));
-        const int nb = (per * 16 + batch - 1) / batch, most = (share < left ? share : left) / batch;
+        const int share = kStepSmem / (step_threads(NT) / NT);
+        const int left = kSmemMost - static_cast<int>(lists_bytes(a.K));
+        const int nb = static_cast<int>((per * 16LL + batch - 1) / batch);
+        const int most = (share < left ? share : left) / batch;
         a.ring = nb < 1 ? 1 : nb < most ? nb : most;
-        return launch_rows(distill_step_kernel<T, NT>, a, NT, step_threads(NT), false, size_t(a.ring) * batch + lists_bytes(a.K),
-                           num_sms, st);
+        return launch_rows(distill_step_kernel<T, NT>, a, NT, step_threads(NT), false,
+                           size_t(a.ring) * batch + lists_bytes(a.K), num_sms, st);
     } else {
         return launch_rows(distill_kernel<T, MODE == kBackward, NT>, a, NT,
                            MODE == kBackward ? gradient_threads(a, static_cast<int>(sizeof(T)), num_sms) : 1024, true,

@@ -673,6 +673,34 @@ def test_offsets_past_32_bits():
     assert (z[:n - 3] == 0).all()
 
 
+def test_a_row_of_more_than_2_30_logits():
+    """Sizes whose bytes pass 32 bits, on one row: the sum in fp64, piece by piece, and the gradient's
+    values at both ends and at the slots."""
+    V = (1 << 30) + 77
+    z = torch.empty(1, V, dtype=BF16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    index = torch.tensor([[5, V - 1, 1 << 29]], device="cuda")
+    teacher = torch.tensor([[1.0, 2.0, 0.5]], device="cuda")
+    m = float(z.max())
+    total = sum(float(torch.exp(z[0, a:a + (1 << 26)].double() - m).sum()) for a in range(0, V, 1 << 26))
+    lse = m + math.log(total)
+    p = torch.softmax(teacher.cpu().double(), 1)
+    zj = z[0, index[0]].double().cpu()
+    want = float((p * (torch.log(p) - (zj - lse))).sum())
+    one = torch.ones(1, device="cuda")
+    loss, stats = rows.distill(z, index, teacher)
+    sl, d = rows.distill_step(z, index, teacher, one)
+    db = rows.distill_backward(z, index, teacher, stats, one)
+    # an exponent of at most 16 in fp32 and V / 2^11 additions per thread of like terms
+    assert abs(float(loss) - want) <= 1e-4 and abs(float(sl) - want) <= 1e-4
+    for g in (d, db):
+        at = torch.cat([torch.arange(3), torch.arange(V - 3, V), index[0].cpu()])
+        ref = torch.exp(z[0, at.cuda()].double().cpu() - lse)
+        for j in range(3):
+            ref[at == index[0, j].item()] -= p[0, j]
+        assert ((g[0, at.cuda()].double().cpu() - ref).abs() <= 2.0 ** -8 * ref.abs() + 1e-4 * ref.abs() + 1e-15).all()
+        assert abs(float(g.double().sum())) <= 2e-3
+
+
 def test_numbers_of_other_types():
     """numpy's numbers, where a Python number is meant."""
     import numpy as np
