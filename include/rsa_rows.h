@@ -36,7 +36,7 @@ extern "C" {
  *   (y_a, y_b) = (n_a cos t - n_b sin t, n_b cos t + n_a sin t),   t = position * freq[i]
  *
  * with the pairs (a, b) = (i, i + rot/2), or (2i, 2i + 1) when interleaved != 0, i < rot/2.
- * Angles are formed and reduced in fp64, so far positions keep their precision.
+ * Angles are formed and reduced in fp64: below 2^31 a position's angle is off by less than 10^-6.
  *
  * Q [B, Hq, L, d], K [B, Hk, L, d] (Hq and Hk independent) and the outputs Qo, Ko of the same
  * shapes: rows contiguous, the other strides in `strides`: (batch, head, row) of Q, K, Qo, Ko,

@@ -122,6 +122,20 @@ def test_qk_gradient_against_differences():
             assert abs((ro.f64(got) * v).sum() - slope) <= 1e-5 * size
 
 
+def test_qk_positions_at_the_end_of_the_range():
+    """Positions near +-2^31: their angles, off by less than 1e-6 each way, stay within the bound."""
+    q, k, w, freq, _, dy = qk_case(8, 1, 2, 2, 64, 64, F32)
+    pos = torch.cat([torch.arange(32) + (1 << 31) - 32, torch.arange(32) - (1 << 31)]).cuda()
+    at = ro.positions_of(64, 0, pos)
+    y = rows.qk_norm_rope(q, k, *w, freq, positions=pos)[0]
+    ref, bound = ro.qk_norm_rope(q, w[0], freq, at, 1e-6, False)
+    ro.check(y, ref, bound, "y")
+    # (pos0 reaches as far: its rows are the positions pos0 + row)
+    y0 = rows.qk_norm_rope(q, k, *w, freq, pos0=(1 << 31) - 64)[0]
+    y1 = rows.qk_norm_rope(q, k, *w, freq, positions=torch.arange(64, device="cuda") + (1 << 31) - 64)[0]
+    assert same(y0, y1)
+
+
 @pytest.mark.parametrize("dt", [BF16, F32])
 def test_qk_in_place_and_into_a_ring_buffer(dt):
     """In place gives the same bits; a rank's keys written into their chunk of the ring's full
