@@ -406,7 +406,10 @@ struct Gradient {
         }
     }
     __device__ __forceinline__ void zeros(const R &rows, const Share &s) const {
-        for (int j = rows.low(s) + threadIdx.x; j < rows.high(s); j += NT) dz[j] = T(0.f);
+        // counted without a sign: a share may end within NT of 2^31
+        T *to = dz + rows.low(s);
+        const unsigned count = rows.high(s) - rows.low(s);
+        for (unsigned j = threadIdx.x; j < count; j += NT) to[j] = T(0.f);
     }
 };
 

@@ -715,6 +715,40 @@ def test_a_row_of_more_than_2_30_logits():
         assert abs(float(g.double().sum())) <= 2e-3
 
 
+def test_rows_of_the_most_logits():
+    """The largest vocabulary, V = 2^31 - 2, of which a row's last columns lie within a block of 2^31:
+    a row without a slot and one with three, of a single row of equal logits that is read for both.
+    q = 1 / V; what lies before and behind the gradient stays."""
+    V, n, pad = (1 << 31) - 2, 2, 4096
+    z = torch.zeros(1, V, dtype=BF16, device="cuda").expand(n, V)
+    index = torch.tensor([[-1, -1, -1], [0, V - 1, V // 2]], device="cuda")
+    teacher, one = torch.zeros(n, 3, device="cuda"), torch.ones(n, device="cuda")
+    buf = torch.empty(pad + n * V + pad, dtype=BF16, device="cuda")
+    d = buf[pad:pad + n * V].view(n, V)
+    # sums of like terms, at most 2^21 of them in a thread: exact before the last few additions
+    want = math.log(V / 3)
+    loss, stats = rows.distill(z, index, teacher)
+    # (and the loss of 20 carries the probabilities' error of 2^-21 of it)
+    assert loss[0] == 0 and abs(float(loss[1]) - want) <= 2e-5
+    assert (stats[0] == 0).all() and abs(float(stats[1, 1]) - math.log(V)) <= 1e-5
+    for step in (False, True):
+        buf.fill_(7)
+        if step:
+            got, _ = rows.distill_step(z, index, teacher, one, dlogits=d)
+            assert same(got, loss)
+        else:
+            rows.distill_backward(z, index, teacher, stats, one, dlogits=d)
+        assert (buf[:pad] == 7).all() and (buf[-pad:] == 7).all()
+        for a in range(0, V, 1 << 28):
+            assert (d[0, a:a + (1 << 28)] == 0).all()
+        at = index[1].sort().values
+        assert ((d[1, at].double() + 1 / 3).abs() <= 2.0 ** -8 / 3 + 1e-6).all()
+        d[1, at] = d[1, 1].clone()
+        assert abs(float(d[1, 1]) * V - 1) <= 2.0 ** -8 + 1e-4
+        for a in range(0, V, 1 << 28):
+            assert (d[1, a:a + (1 << 28)] == d[1, 1]).all()
+
+
 def test_numbers_of_other_types():
     """numpy's numbers, where a Python number is meant."""
     import numpy as np
