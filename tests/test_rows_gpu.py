@@ -178,6 +178,44 @@ def test_qk_rows_stand_alone():
         assert same(t[0][keep], t0[0][keep])
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_qk_rows_whose_squares_overflow(dt, inter):
+    """Rows of finite numbers: where the sum of squares passes the largest fp32 number, zeros, and
+    zero gradients that leave the weights' alone; where only the products with weights, factors or
+    gradients could pass it, the formula's values."""
+    q, k, w, freq, pos, dy = qk_case(9, 1, 3, 3, 40, 64, dt, positions="row64")
+    w = [t.abs() + 1 for t in w]
+    most = torch.finfo(dt).max
+    gone = {2: 1e20, 5: most, 7: -most, 11: 3e19}  # row: its size
+    for s, (x, g) in enumerate(zip((q, k), dy)):
+        for l, size in gone.items():
+            x[0, s, l] = size
+        x[0, s, 13, ::3] = most      # (some of the row)
+        x[0, 2, 17] *= 3e17          # 64 squares of at most 1e37 each
+        x[0, 2, 18] *= 3e17
+        x[0, 1, 23] *= 1e17
+        g[0, 2, 18] *= 1e24          # and products of 1e42
+        g[0, 1, 24] *= 1e30
+    out = [(x[0, s, l]) for s, x in enumerate((q, k)) for l in (*gone, 13)]
+    assert all(torch.isfinite(t).all() and torch.isinf((t.float() ** 2).sum()) for t in out)
+    assert all(torch.isfinite((x[0, 2, 17:19].float() ** 2).sum(-1)).all() for x in (q, k))
+    y = rows.qk_norm_rope(q, k, *w, freq, positions=pos, interleaved=inter)
+    grads = rows.qk_norm_rope_backward(q, k, *dy, *w, freq, positions=pos, interleaved=inter)
+    at = ro.positions_of(40, 0, pos)
+    for s, x in enumerate((q, k)):
+        keep = torch.ones(3, 40, dtype=torch.bool)
+        keep[s, [*gone, 13]] = False
+        x0, g0 = x.clone(), dy[s].clone()
+        x0[0][~keep.cuda()], g0[0][~keep.cuda()] = 0, 0
+        ref, bound = ro.qk_norm_rope(x0, w[s], freq, at, 1e-6, inter)
+        ro.check(y[s], ref, bound, f"y[{s}]")
+        dx, dx_bound, dw, dw_bound = ro.qk_norm_rope_backward(x0, w[s], freq, at, g0, 1e-6, inter)
+        ro.check(grads[s], dx, dx_bound, f"dx[{s}]")
+        ro.check(grads[2 + s], dw, dw_bound, f"dw[{s}]")
+        assert (y[s][0][~keep.cuda()] == 0).all() and (grads[s][0][~keep.cuda()] == 0).all()
+
+
 def test_qk_without_rows():
     q = torch.empty(2, 3, 0, 64, dtype=BF16, device="cuda")
     w = torch.ones(64, device="cuda")
