@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, kQkBlocksPerSm) qk_norm_bwd_kernel(c
             ux[0] = add2(ux[0], ux[1]);
             const float s1 = row_sum<LPR>(ss[0].x + ss[0].y), s2 = row_sum<LPR>(ux[0].x + ux[0].y);
             const float r = rsqrtf(s1 * (1.f / D) + a.eps);
-            float q = -r * r * s2 * (1.f / D);
+            float q = -r * (r * s2) * (1.f / D);  // (r s2 is of the size of u, r r need not be finite)
             // Numbers so large that s2 overflowed (and r may be 0): the sum once more, of r x. The
             // shuffles are the whole warp's (by the row's lanes alone, in a branch of their own: 75 us
             // instead of 70), the result is taken by the rows concerned.

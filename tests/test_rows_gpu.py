@@ -216,6 +216,23 @@ def test_qk_rows_whose_squares_overflow(dt, inter):
         assert (y[s][0][~keep.cuda()] == 0).all() and (grads[s][0][~keep.cuda()] == 0).all()
 
 
+@pytest.mark.parametrize("eps", [1e-40, 1e-30, 1.0])
+def test_qk_eps_of_any_size(eps):
+    """A row of zeros beside ordinary ones: dx = eps^(-1/2) u, whose square root's square may pass
+    the largest fp32 number."""
+    eps = float(torch.tensor(eps))  # as the kernel has it
+    q, k, w, freq, _, dy = qk_case(10, 1, 2, 1, 9, 64, F32)
+    q[0, 1, 4] = 0
+    y = rows.qk_norm_rope(q, k, *w, freq, eps=eps)[0]
+    dx, _, dw, _ = rows.qk_norm_rope_backward(q, k, *dy, *w, freq, eps=eps)
+    at = ro.positions_of(9, 0, None)
+    ref, bound = ro.qk_norm_rope(q, w[0], freq, at, eps, False)
+    ro.check(y, ref, bound, "y")
+    ref, bound, dw_ref, dw_bound = ro.qk_norm_rope_backward(q, w[0], freq, at, dy[0], eps, False)
+    ro.check(dx, ref, bound, "dx")
+    ro.check(dw, dw_ref, dw_bound, "dw")
+
+
 def test_qk_without_rows():
     q = torch.empty(2, 3, 0, 64, dtype=BF16, device="cuda")
     w = torch.ones(64, device="cuda")
