@@ -245,15 +245,16 @@ struct Rows {
             if (slots(place)[j] >= 0) t = join(t, {probs(place)[j], 1.f}, c);
         return t;
     }
-    // The thread's slots of a row: probabilities into the lists, and its part of the loss in base
-    // 2 (m, logsum: the row's maximum and log2 of its sum).
+    // The thread's slots of a row: probabilities into the lists, and its part of the loss over tau
+    // (m, logsum: the row's maximum and log2 of its sum): p (tau (ln p + ln sum) - (z - m)), in which
+    // a logit of the type's lowest value is not scaled before its probability has made it small.
     __device__ __forceinline__ float finish_slots(int place, MaxSum t, float m, float logsum) const {
-        const float tl2 = log2f(t.s);
+        const float tl2 = log2f(t.s), nat = a.tau * kLn2;
         float l = 0.f;
         for (int j = threadIdx.x; j < Kp; j += NT) {
             const float lp = (probs(place)[j] - t.m) * c - tl2;  // log2 p
             const float p = slots(place)[j] >= 0 ? exp2_ftz(lp) : 0.f;
-            if (p != 0.f) l += p * (lp - ((logits(place)[j] - m) * c - logsum));
+            if (p != 0.f) l += p * (nat * (lp + logsum) - (logits(place)[j] - m));
             probs(place)[j] = p;
         }
         return l;
@@ -416,13 +417,13 @@ struct Gradient {
 enum { kForward, kBackward, kStep };
 constexpr int kPlaces = 4;  // rows whose lists are in use between two barriers, and one more
 
-// Sum of the warps' parts of a row's loss, in the loss's units.
+// Sum of the warps' parts of a row's loss over tau, as the loss.
 template <int W>
 __device__ __forceinline__ float row_loss(const float (&part)[W], float tau) {
     float l = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) l += part[w];
-    return tau * tau * kLn2 * l;
+    return tau * l;
 }
 
 __device__ __forceinline__ float warp_sum(float x) {

@@ -553,6 +553,27 @@ def test_distill_special_rows():
     assert torch.isnan(loss[6]) and torch.isnan(loss[7]) and not torch.isnan(loss[0])
 
 
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("tau", [0.5, 1.0, 2.0])
+def test_distill_slot_at_the_lowest_value(dt, tau):
+    """The teacher gives mass to an entry that holds the type's lowest value (an entry not in
+    use): the loss is about tau p 3.4e38, which fp32 holds."""
+    z, index, teacher, dloss = distill_case(12, 6, 900, 5, dt, pad=False)
+    for r in range(5):
+        index[r] = torch.arange(5) * 7 + r
+        z[r, index[r, r]] = torch.finfo(dt).min
+    teacher[:] = torch.tensor([0.2, 0.1, 0.0, -0.1, 0.3])
+    ref, bound, _, _ = ro.distill(z, index, teacher, tau)
+    assert (ref[:5] > 1e36).all() and (ref < 3e38).all()
+    loss, stats = rows.distill(z, index, teacher, tau)
+    ro.check(loss, ref, bound, "loss")
+    sl, d = rows.distill_step(z, index, teacher, dloss, tau)
+    ro.check(sl, ref, bound, "step's loss")
+    dref, dbound = ro.distill_backward(z, index, teacher, dloss, tau)
+    ro.check(d, dref, dbound, "step's dlogits")
+    ro.check(rows.distill_backward(z, index, teacher, stats, dloss, tau), dref, dbound, "dlogits")
+
+
 def test_distill_is_cross_entropy_with_one_slot():
     z, index, _, dloss = distill_case(9, 50, 777, 1, F32, pad=False)
     loss, _ = rows.distill(z, index, torch.zeros(50, 1, device="cuda"))
