@@ -487,6 +487,41 @@ def test_distill(case):
     assert same(rows.distill_step(z2, index, teacher, dloss, tau, dlogits=z2)[1], sd)
 
 
+# Several rows per CTA, live and padded ones in turn, through every number of threads: rows that
+# shared memory cannot hold whole in one pass (512 threads; 256, 128 and 64 with a little too much for
+# their share), and the two passes' ring refilled by CTAs of 64 threads.
+DISTILL_MANY = [
+    (300, 131072, 128, BF16, 1.0),
+    (310, 100003, 33, BF16, 2.0),
+    (200, 60001, 20, F32, 1.0),
+    (1000, 33501, 20, BF16, 1.0),
+    (1100, 8401, 40, F32, 0.5),
+    (2400, 8451, 9, BF16, 1.0),
+    (2400, 20001, 16, BF16, 1.0),
+]
+
+
+@pytest.mark.parametrize("case", DISTILL_MANY, ids=lambda c: "-".join(str(x).replace("torch.", "") for x in c))
+def test_distill_many_rows(case):
+    n, V, K, dt, tau = case
+    z, index, teacher, dloss = distill_case(n, n, V, K, dt)
+    loss, stats = rows.distill(z, index, teacher, tau)
+    dz = rows.distill_backward(z, index, teacher, stats, dloss, tau)
+    sl, sd = rows.distill_step(z, index, teacher, dloss, tau)
+    z1, z2 = z.clone(), z.clone()
+    assert same(rows.distill_backward(z1, index, teacher, stats, dloss, tau, dlogits=z1), dz)
+    assert same(rows.distill_step(z2, index, teacher, dloss, tau, dlogits=z2)[1], sd)
+    for a in range(0, n, 128):
+        part = [t[a:a + 128] for t in (z, index, teacher)]
+        ref, bound, sref, sbound = ro.distill(*part, tau)
+        ro.check(loss[a:a + 128], ref, bound, f"loss from {a}")
+        ro.check(sl[a:a + 128], ref, bound, f"step's loss from {a}")
+        ro.check(stats[a:a + 128], sref, sbound, f"stats from {a}")
+        ref, bound = ro.distill_backward(*part, dloss[a:a + 128], tau)
+        ro.check(dz[a:a + 128], ref, bound, f"dlogits from {a}")
+        ro.check(sd[a:a + 128], ref, bound, f"step's dlogits from {a}")
+
+
 @pytest.mark.parametrize("dt", [BF16, F32])
 @pytest.mark.parametrize("lo,dlo", [(0, 0), (1, 1), (3, 0), (5, 2)])
 def test_distill_layouts(dt, lo, dlo):
