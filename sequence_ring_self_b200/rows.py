@@ -243,12 +243,14 @@ def _vector_rows(t):
 
 class QKNormRope(torch.autograd.Function):
     """autograd wrapper: ``QKNormRope.apply(q, k, wq, wk, freq, positions, pos0, eps,
-    interleaved)`` -> (q', k'). Gradients for q, k, wq and wk."""
+    interleaved)`` -> (q', k'). Gradients for q, k, wq and wk. Queries, keys and gradients whose rows
+    are not contiguous and 16-byte aligned are copied."""
 
     @staticmethod
     def forward(ctx, q, k, wq, wk, freq, positions=None, pos0=0, eps=1e-6, interleaved=False):
         if ctx.needs_input_grad[4]:
             raise ValueError("freq has no gradient here; detach it")
+        q, k = (t if t.dim() != 4 or _vector_rows(t) else t.contiguous() for t in (q, k))
         ctx.save_for_backward(q, k, wq, wk, freq, positions)
         ctx.rest = dict(pos0=pos0, eps=eps, interleaved=interleaved)
         return qk_norm_rope(q, k, wq, wk, freq, positions=positions, **ctx.rest)
@@ -294,7 +296,7 @@ def _flat(name, t, D):
 
 
 def embed(ids, table, scale: float = 1.0, *, out=None, stream: torch.cuda.Stream | None = None):
-    """``scale * table[ids]``: ids int64 or int32 of any shape, table [V, D] bf16 or fp32 (rows
+    """``scale * table[ids]``: ids int64 or int32 of any shape, contiguous, table [V, D] bf16 or fp32 (rows
     contiguous, any distance apart). An id outside [0, V) gives a row of zeros. Returns
     [*ids.shape, D] in the table's type."""
     i64, dt, n = _ids_checked(ids), _dtype(table), ids.numel()
@@ -359,10 +361,12 @@ def embed_workspace_size(n: int, num_rows: int, D: int) -> int:
 
 
 class Embedding(torch.autograd.Function):
-    """autograd wrapper: ``Embedding.apply(ids, table, scale)`` -> rows."""
+    """autograd wrapper: ``Embedding.apply(ids, table, scale)`` -> rows. ids may be strided (a copy
+    is made)."""
 
     @staticmethod
     def forward(ctx, ids, table, scale=1.0):
+        ids = ids.contiguous()
         ctx.save_for_backward(ids)
         ctx.scale, ctx.V = scale, table.shape[0]
         return embed(ids, table, scale)
@@ -397,6 +401,16 @@ def _distill_checked(logits, index, teacher, temperature, *more):
     return device, shape[:-1], head, (n, V, K, float(temperature), dt)
 
 
+def _as_rows(t):
+    """t, copied if its rows are not contiguous and the same distance apart."""
+    try:
+        if t.dim() > 1:
+            _ld(_flat("t", t, t.shape[-1]))
+        return t
+    except ValueError:
+        return t.contiguous()
+
+
 def _rows_of(name, t, shape):
     """fp32 values of the rows: 1 (elements apart) for a contiguous tensor of the rows' shape, 0
     for an expanded one or a single value for all rows."""
@@ -422,7 +436,8 @@ def distill(logits, index, teacher, temperature: float = 1.0, *, loss=None, stat
             stream: torch.cuda.Stream | None = None):
     """Distillation loss of each row of the student's logits [..., V] against the teacher's K
     largest logits: index [..., K] (int64 or int32; outside [0, V): an empty slot) and teacher
-    [..., K] (bf16 or fp32; -inf: an empty slot). With p = softmax(teacher / temperature) over the
+    [..., K] (bf16 or fp32; -inf: an empty slot), both contiguous; the rows of the logits are
+    contiguous and the same distance apart. With p = softmax(teacher / temperature) over the
     slots and q = softmax(logits / temperature): temperature^2 * sum p (ln p - ln q). A row of
     empty slots has loss 0. With K = 1 this is the cross entropy with index as the label, times
     temperature^2. Returns (loss [...] fp32, stats [..., 2] fp32 = (max logit,
@@ -488,12 +503,16 @@ def distill_step(logits, index, teacher, dloss, temperature: float = 1.0, *, los
 
 class Distill(torch.autograd.Function):
     """autograd wrapper: ``Distill.apply(logits, index, teacher, temperature)`` -> loss per row.
-    Gradient for the logits alone."""
+    Gradient for the logits alone. Strided index and teacher are copied, and so are logits whose
+    rows are not the same distance apart, as ``logits[:, :-1]`` of several sequences: there, an
+    index of -1 in the last position (a row without a slot has no loss and no gradient) saves the
+    copy."""
 
     @staticmethod
     def forward(ctx, logits, index, teacher, temperature=1.0):
         if ctx.needs_input_grad[2]:
             raise ValueError("the teacher has no gradient here; detach it")
+        logits, index, teacher = _as_rows(logits), index.contiguous(), teacher.contiguous()
         loss, stats = distill(logits, index, teacher, temperature)
         ctx.save_for_backward(logits, index, teacher, stats)
         ctx.temperature = temperature

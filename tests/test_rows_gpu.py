@@ -398,6 +398,47 @@ def test_embed_backward_edges():
     assert (out[0] == 50).all() and (out[1] == 0).all()
 
 
+def test_autograd_takes_shifted_and_unaligned_inputs():
+    """The wrappers on slices of a batch of sequences (tokens and logits without the last position,
+    labels without the first) and on rows off 16-byte boundaries: the same bits, forward and
+    backward, as on contiguous copies."""
+    g = gen(22)
+    B, L, V, K, d = 3, 14, 333, 5, 64
+
+    def both_ways(fn, views, grads_of):
+        out = []
+        for copy in (False, True):
+            base = [t.clone().requires_grad_(i in grads_of) for i, (t, _) in enumerate(views)]
+            args = [v(b) for b, (_, v) in zip(base, views)]
+            if copy:
+                args = [a.contiguous() if a is not None else a for a in args]
+            y = fn(*args)
+            y = y if isinstance(y, tuple) else (y,)
+            gy = [randn(gen(23 + i), *t.shape, dt=t.dtype) for i, t in enumerate(y)]
+            torch.autograd.backward(y, gy)
+            out.append([t.detach() for t in y] + [base[i].grad for i in grads_of])
+        assert len(out[0]) == len(out[1]) and all(same(a, b) for a, b in zip(*out))
+
+    ids = torch.randint(-1, 51, (B, L), generator=g).cuda()
+    both_ways(lambda i, t: rows.Embedding.apply(i, t, 2.0),
+              [(ids, lambda t: t[:, :-1]), (randn(g, 50, 24), lambda t: t)], (1,))
+    z, index = randn(g, B, L, V), torch.randint(-1, V, (B, L, K), generator=g).cuda()
+    for cut in (lambda t: t[:, :-1], lambda t: t.transpose(1, 2)[:, :, :-1].transpose(1, 2), lambda t: t[:1, :-1]):
+        both_ways(lambda *a: rows.Distill.apply(*a, 2.0),
+                  [(z, cut), (index, lambda t: t[:, 1:][:cut(z).shape[0]]),
+                   (randn(g, B, L, K), lambda t: t[:, 1:][:cut(z).shape[0]])], (0,))
+    both_ways(lambda *a: rows.Distill.apply(*a, 2.0),
+              [(randn(g, V, L), lambda t: t.T), (index[0].clone(), lambda t: t), (randn(g, L, K), lambda t: t)], (0,))
+    freq, w = torch.rand(32, generator=g).cuda(), randn(g, d)
+    for dt in (BF16, F32):
+        both_ways(lambda q, k, w: rows.QKNormRope.apply(q, k, w, None, freq, None, 5),
+                  [(randn(g, B, 2, L, d + 1, dt=dt), lambda t: t[..., 1:]),
+                   (randn(g, B, 2, L, d + 1, dt=dt), lambda t: t[..., :d]), (w, lambda t: t)], (0, 1, 2))
+        both_ways(lambda q, k: rows.QKNormRope.apply(q, k, None, None, freq),
+                  [(randn(g, B, 2, d, L, dt=dt), lambda t: t.transpose(2, 3)),
+                   (randn(g, B, 2, L, d, dt=dt), lambda t: t)], (0, 1))
+
+
 def test_embedding_autograd_and_differences():
     """The operator is linear in the table, so a difference is exact up to rounding."""
     g = gen(21)

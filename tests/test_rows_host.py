@@ -177,6 +177,21 @@ def test_binding_refuses_before_it_calls():
         rows.distill(z.double(), i, t)
 
 
+def test_autograd_wrappers_copy_what_the_functions_refuse():
+    """Strided ids, slots and rows pass the wrappers and are refused by the functions (here both end
+    at the check for a GPU)."""
+    ids, table = torch.zeros(2, 5, dtype=torch.int64)[:, :-1], torch.zeros(5, 8)
+    z, i, t = torch.zeros(2, 5, 9)[:, :-1], torch.zeros(2, 5, 3, dtype=torch.int64)[:, 1:], torch.zeros(2, 5, 3)[:, 1:]
+    with pytest.raises(ValueError, match="contiguous"):
+        rows.embed(ids, table)
+    with pytest.raises(ValueError, match="CUDA"):
+        rows.Embedding.apply(ids, table)
+    with pytest.raises(ValueError, match="contiguous"):
+        rows.distill(z, i, t)
+    with pytest.raises(ValueError, match="CUDA"):
+        rows.Distill.apply(z, i, t)
+
+
 def test_plain_forms_against_differentiation():
     """The plain gradients that the GPU is held against agree with differentiating the plain
     forward passes (fp64, so to about 1e-12)."""
