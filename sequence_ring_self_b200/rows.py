@@ -28,6 +28,7 @@ from functools import lru_cache
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from . import rsa
 
@@ -38,10 +39,11 @@ _DT = {torch.bfloat16: rsa.RSA_BF16, torch.float32: rsa.RSA_F32}
 _S12, _S18 = ctypes.c_longlong * 12, ctypes.c_longlong * 18
 
 
-def _call(name, device, stream, tensors, body):
+def _call(name, device, stream, tensors, written, body):
     """Runs ``body(lib, stream handle)`` with the tensors' device current and, where `stream` is
     not the current one, with its allocations made for `stream`. `body` returns the status code
-    and the result."""
+    and the result. The tensors given as outputs, `written`, count as modified in place, so that
+    autograd does not take them for what it saved."""
     lib = rsa._lib or rsa.load_library()
     if stream is None and device.index == torch.cuda.current_device():
         # the current stream's handle, without building a Stream object around it
@@ -59,6 +61,9 @@ def _call(name, device, stream, tensors, body):
                     t.record_stream(s)
     if rc != rsa.RSA_OK:
         raise rsa.RSAError(rc, name)
+    for t in written:
+        if t is not None:
+            increment_version(t)
     return out
 
 
@@ -189,7 +194,7 @@ def qk_norm_rope(q, k, wq, wk, freq, *, pos0: int = 0, positions=None, eps: floa
         return rc, (oq, ok)
 
     return _call("rsa_qk_norm_rope", device, stream, (q, k, wq, wk, freq, positions, out_q, out_k),
-                 body)
+                 (out_q, out_k), body)
 
 
 def qk_norm_rope_backward(q, k, dq_out, dk_out, wq, wk, freq, *, pos0: int = 0, positions=None,
@@ -221,7 +226,7 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, wq, wk, freq, *, pos0: int = 0, 
         return rc, (gq, gk, dwq, dwk)
 
     return _call("rsa_qk_norm_rope_backward", device, stream,
-                 (q, k, dq_out, dk_out, wq, wk, freq, positions, dq, dk, workspace), body)
+                 (q, k, dq_out, dk_out, wq, wk, freq, positions, dq, dk, workspace), (dq, dk), body)
 
 
 def qk_norm_rope_workspace_size(d: int) -> int:
@@ -296,8 +301,8 @@ def _flat(name, t, D):
 
 
 def embed(ids, table, scale: float = 1.0, *, out=None, stream: torch.cuda.Stream | None = None):
-    """``scale * table[ids]``: ids int64 or int32 of any shape, contiguous, table [V, D] bf16 or fp32 (rows
-    contiguous, any distance apart). An id outside [0, V) gives a row of zeros. Returns
+    """``scale * table[ids]``: ids int64 or int32 of any shape, contiguous, table [V, D] bf16 or fp32
+    (rows contiguous, any distance apart). An id outside [0, V) gives a row of zeros. Returns
     [*ids.shape, D] in the table's type."""
     i64, dt, n = _ids_checked(ids), _dtype(table), ids.numel()
     if table.dim() != 2:
@@ -317,7 +322,7 @@ def embed(ids, table, scale: float = 1.0, *, out=None, stream: torch.cuda.Stream
                            float(scale), dt, s)
         return rc, o
 
-    return _call("rsa_embed", device, stream, (ids, table, out), body)
+    return _call("rsa_embed", device, stream, (ids, table, out), (out,), body)
 
 
 def embed_backward(ids, dout, num_rows: int, scale: float = 1.0, *, dtable=None,
@@ -351,7 +356,7 @@ def embed_backward(ids, dout, num_rows: int, scale: float = 1.0, *, dtable=None,
                                     _nbytes(ws), s)
         return rc, dtab
 
-    return _call("rsa_embed_backward", device, stream, (ids, dout, dtable, workspace), body)
+    return _call("rsa_embed_backward", device, stream, (ids, dout, dtable, workspace), (dtable,), body)
 
 
 def embed_workspace_size(n: int, num_rows: int, D: int) -> int:
@@ -451,7 +456,8 @@ def distill(logits, index, teacher, temperature: float = 1.0, *, loss=None, stat
         sa = lo.new_empty((*shape, 2)) if stats is None else stats
         return lib.rsa_distill(*head, lo.data_ptr(), sa.data_ptr(), *sizes, s), (lo, sa)
 
-    return _call("rsa_distill", device, stream, (logits, index, teacher, loss, stats), body)
+    return _call("rsa_distill", device, stream, (logits, index, teacher, loss, stats),
+                 (loss, stats), body)
 
 
 def _gradient(logits, dlogits):
@@ -478,7 +484,7 @@ def distill_backward(logits, index, teacher, stats, dloss, temperature: float = 
                                         *sizes, s), out
 
     return _call("rsa_distill_backward", device, stream,
-                 (logits, index, teacher, stats, dloss, dlogits), body)
+                 (logits, index, teacher, stats, dloss, dlogits), (dlogits,), body)
 
 
 def distill_step(logits, index, teacher, dloss, temperature: float = 1.0, *, loss=None,
@@ -498,7 +504,7 @@ def distill_step(logits, index, teacher, dloss, temperature: float = 1.0, *, los
                                     s), (lo, out)
 
     return _call("rsa_distill_step", device, stream,
-                 (logits, index, teacher, dloss, loss, dlogits), body)
+                 (logits, index, teacher, dloss, loss, dlogits), (loss, dlogits), body)
 
 
 class Distill(torch.autograd.Function):

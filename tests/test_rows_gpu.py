@@ -439,6 +439,37 @@ def test_autograd_takes_shifted_and_unaligned_inputs():
                    (randn(g, B, 2, L, d, dt=dt), lambda t: t)], (0, 1))
 
 
+def test_outputs_written_in_place_are_known_to_autograd():
+    """A tensor that an operator overwrites counts as modified: a backward pass that saved it refuses
+    to run on the new contents."""
+    z, index, teacher, dloss = distill_case(24, 6, 100, 4, F32)
+    leaf = z.clone().requires_grad_()
+    logits = leaf * 1
+    loss = rows.Distill.apply(logits, index, teacher, 1.0)
+    rows.distill_step(logits.detach(), index, teacher, dloss, dlogits=logits.detach())
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.sum().backward()
+    q, k, w, freq, _, dy = qk_case(25, 1, 2, 2, 9, 64, F32)
+    table, ids, dout = randn(gen(26), 10, 8), torch.arange(5, device="cuda"), randn(gen(27), 5, 8)
+    out, dtable, lo, st = dout.clone(), table.clone(), dloss.clone(), torch.empty(6, 2, device="cuda")
+    stats = rows.distill(z, index, teacher)[1]
+    calls = [
+        ((q, k), lambda: rows.qk_norm_rope(q, k, *w, freq, out_q=q, out_k=k)),
+        ((dy[0], dy[1]), lambda: rows.qk_norm_rope_backward(q, k, *dy, *w, freq, dq=dy[0], dk=dy[1])),
+        ((out,), lambda: rows.embed(ids, table, out=out)),
+        ((dtable,), lambda: rows.embed_backward(ids, dout, 10, dtable=dtable, accumulate=True)),
+        ((lo, st), lambda: rows.distill(z, index, teacher, loss=lo, stats=st)),
+        ((z,), lambda: rows.distill_backward(z, index, teacher, stats, dloss, dlogits=z)),
+        ((z, lo), lambda: rows.distill_step(z, index, teacher, dloss, dlogits=z, loss=lo))]
+    read = [index, teacher, dloss, stats, ids, table, dout, *w, freq]
+    before = [t._version for t in read]
+    for written, call in calls:
+        versions = [t._version for t in written]
+        call()
+        assert all(t._version > v for t, v in zip(written, versions))
+    assert [t._version for t in read] == before
+
+
 def test_embedding_autograd_and_differences():
     """The operator is linear in the table, so a difference is exact up to rounding."""
     g = gen(21)
