@@ -75,6 +75,66 @@ def test_every_rank_rotates_by_the_position_in_the_sequence():
     np.testing.assert_allclose(run_ranks(2), run_ranks(1), rtol=0, atol=1e-10)
 
 
+def fp64_embed(ids, table, scale):
+    live = (ids >= 0) & (ids < len(table))
+    return torch.where(live[:, None], table[torch.where(live, ids, 0)] * scale, 0.0)
+
+
+def _model_worker(rank, world, port, out):
+    os.environ.update(RANK=str(rank), WORLD_SIZE=str(world), MASTER_ADDR="127.0.0.1", MASTER_PORT=str(port))
+    import torch.distributed as dist
+
+    dist.init_process_group("gloo", timeout=datetime.timedelta(seconds=60))
+    try:
+        s, V, Vp = SHAPE, 45, 48
+        to = lambda a, bias=False: torch.from_numpy(a.copy())
+        blocks = [with_norm(_weights(block_inputs(s["L"], s["hidden"], s["H"], s["d"], s["ffn"], seed=940 + i),
+                                     s["H"], s["d"], to), s["d"]) for i in range(2)]
+        blocks[1].freq = None  # the norm alone, and further down neither
+        blocks.append(_weights(block_inputs(s["L"], s["hidden"], s["H"], s["d"], s["ffn"], seed=942), s["H"],
+                               s["d"], to))
+        g = torch.Generator().manual_seed(5)
+        wts = block.ModelWeights(table=torch.randn(V, s["hidden"], generator=g, dtype=torch.float64), blocks=blocks,
+                                 head=torch.randn(Vp, s["hidden"], generator=g, dtype=torch.float64), vocab=V,
+                                 scale=1.5)
+        ids = torch.randint(-1, V + 1, (s["L"],), generator=g)
+        c = s["L"] // world
+        z = block.model_forward(ids[rank * c:(rank + 1) * c], wts, ring=ring.DistRing(), comp=Fp64Steps(),
+                                lin=fp64_linear, qk=fp64_qk_or_norm, embed=fp64_embed)
+        out.put((rank, z.numpy()))
+    finally:
+        dist.destroy_process_group()
+
+
+def fp64_qk_or_norm(q, k, wts, pos0):
+    """fp64_qk for a block that may have no frequencies."""
+    if wts.freq is not None:
+        return fp64_qk(q, k, wts, pos0)
+    return tuple(x / torch.sqrt((x * x).mean(-1, keepdim=True) + wts.norm_eps) * w
+                 for x, w in ((q, wts.wq_norm), (k, wts.wk_norm)))
+
+
+def run_model_ranks(world):
+    ctx = mp.get_context("spawn")
+    q, port = ctx.Queue(), _free_port()
+    procs = [ctx.Process(target=_model_worker, args=(r, world, port, q)) for r in range(world)]
+    for p in procs:
+        p.start()
+    res = dict(q.get(timeout=180) for _ in range(world))
+    for p in procs:
+        p.join(timeout=60)
+        assert p.exitcode == 0
+    return np.concatenate([res[r] for r in range(world)])
+
+
+def test_a_model_on_several_ranks_has_the_logits_of_one():
+    """Tokens in chunks over gloo ranks: embedding, blocks and head on the rank's rows, every row's
+    logits as on one rank, without the head's padded columns."""
+    one = run_model_ranks(1)
+    assert one.shape == (SHAPE["L"], 45)
+    np.testing.assert_allclose(run_model_ranks(2), one, rtol=0, atol=1e-9 * np.abs(one).max())
+
+
 class _Alone:
     """A ring of one rank, for a block on a whole sequence."""
     rank, world = 0, 1
