@@ -36,7 +36,8 @@ extern "C" {
  *   (y_a, y_b) = (n_a cos t - n_b sin t, n_b cos t + n_a sin t),   t = position * freq[i]
  *
  * with the pairs (a, b) = (i, i + rot/2), or (2i, 2i + 1) when interleaved != 0, i < rot/2.
- * Angles are formed and reduced in fp64: below 2^31 a position's angle is off by less than 10^-6.
+ * Angles are formed and reduced in fp64: off by less than 3 * 2^-53 |position * freq| + 2^-23, which is
+ * less than 10^-6 while |position * freq| stays below 2^31.
  *
  * Q [B, Hq, L, d], K [B, Hk, L, d] (Hq and Hk independent) and the outputs Qo, Ko of the same
  * shapes: rows contiguous, the other strides in `strides`: (batch, head, row) of Q, K, Qo, Ko,
@@ -125,6 +126,8 @@ RSA_API rsa_status_t rsa_embed_backward(const void *ids, int ids64, const void *
  * gradient 0, whatever its logits. z may hold -infinity or the type's lowest value (entries not
  * in use); a row whose every logit is -infinity, or that holds a NaN, gives NaN.
  * stats[t] = (max z, ln sum exp((z - max) / tau)): what the backward pass needs.
+ * In fp32 the loss is off by about 10^-6 tau^2 (1 + ln V): more than the loss itself where tau is large
+ * and the live slots are nearly the whole vocabulary.
  *
  * logits [n, V], rows ld elements apart, type dt; index [n, K] int64 (index64 != 0) or int32;
  * teacher [n, K] of type teacher_dt; loss fp32 [n]; stats fp32 [n, 2] (8-byte aligned). Logits

@@ -13,7 +13,8 @@
 // and the few columns with a teacher's slot are written once more afterwards, from logits read
 // before anything of the row was written (which lets the gradient replace the logits in place).
 // One block barrier per row: it makes the row's sums whole, the last row's slots visible, and
-// tells whether the next row has a slot at all (a row without one is not read).
+// tells whether the next row has a slot at all. Nothing of a row without one is used, but a CTA's
+// first row, and in one pass the beginning of every next row, is sent for before that is known.
 #include <cooperative_groups.h>
 #include <type_traits>
 
@@ -651,8 +652,9 @@ __global__ void __launch_bounds__(NT, step_threads(NT) / NT) distill_step_kernel
         }
 
         if (has_next && tid == 0) {
-            // the next row on its way to L2 while this one is brought to its end (sent for at the
-            // start of the row it pushes out what is still to be read: 571 us instead of 469)
+            // the next row, or what kStepAhead holds of it, on its way to L2 while this one is brought
+            // to its end, whether or not it turns out to have a slot (sent for at the start of the row
+            // it pushes out what is still to be read: 571 us instead of 469)
             const typename R::Share next = rows.share_of(next_row);
             const int bytes = min(next.n, kStepAhead / 16) * 16;
             if (bytes)
@@ -731,7 +733,9 @@ cudaError_t launch_rows(Kernel kernel, const DistillArgs &a, int nt, int threads
 constexpr int kStepSmem = 200 * 1024, kSmemMost = 224 * 1024;  // (227 KB less the static part)
 
 // Threads per SM of the gradient's pass. Many long rows: half of what fits, which leaves DRAM longer
-// runs (4096 rows of 32768 bf16 logits: 101 us instead of 110; the loss alone takes 59 instead of
+// runs (4096 rows of 32768 bf16 logits: 98 us instead of 105; of 16384: 52 either way. Shorter or
+// fewer rows want all: 25 instead of 32 for 4096 rows of 8192, 40 instead of 42 for 1000 of 50001,
+// 37 instead of 39 for 1500 of 32768; the loss alone of 4096 rows of 32768 takes 59 instead of
 // 52 that way).
 int gradient_threads(const DistillArgs &a, int size, int num_sms) {
     return a.n >= 16 * num_sms && static_cast<long long>(a.V) * size >= 32768 ? 512 : 1024;

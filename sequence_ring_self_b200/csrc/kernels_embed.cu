@@ -74,7 +74,7 @@ constexpr int kSortKeep = 4;  // rounds of 32 tokens that a warp loads at once
 // CTAs and digits through distributed shared memory, and the warps place their tokens in
 // order. The lists lie in global memory (in practice in L2); the cluster's barriers order the
 // passes. Ids outside [0, V) become V and sort last. Bound by latency: about five dependent trips
-// to L2 or a neighbouring SM per pass (10 us for 16384 tokens).
+// to L2 or a neighbouring SM per pass (alone: 10.5 us for 8192 tokens, 15 for 16384).
 //
 // Unless the sums are added to what is there, the grid has more clusters, which meanwhile fill the
 // gradient with zeros in accesses of N elements, a row per warp (as a kernel of its own beside
@@ -458,9 +458,10 @@ void embed_sort_plan(EmbedArgs &a) {
 }
 
 // CTAs of the sort: a round of 32 tokens costs a warp more than the cluster's barriers do, so one
-// round each up to four CTAs, eight for more than 4096 tokens (four rounds at 8192 tokens: 23.4 us
-// for the whole gradient instead of 20.6; eight CTAs at 4096: 21.3 instead of 17.9). The zeros
-// take the other SMs, or with clusters seven eighths of all (so that every cluster finds its
+// round each up to four CTAs, eight for more than 4096 tokens (the whole gradient of 30000 x 768
+// bf16 from 8192 tokens: 29.4 us with four, 26.9 with eight; from 16384 tokens 43.8 and 33.9; from
+// 4096, 21.0 and 22.8; added to a table, without the zeros' clusters, 26.0 and 22.6, 49.5 and 37.9,
+// 19.2 and 17.9). The zeros take the other SMs, or with clusters seven eighths of all (so that every cluster finds its
 // place at once: 55 us instead of 62 for a 32768 x 2048 bf16 table).
 cudaError_t launch_embed_sort(EmbedArgs a, int bf16_out, int vec, int num_sms, cudaStream_t st) {
     a.sort_ctas = 1;

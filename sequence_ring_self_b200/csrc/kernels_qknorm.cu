@@ -30,7 +30,8 @@ __device__ __forceinline__ double turns_per_unit(long long pos) {
 }
 
 // (cos, sin) of position * freq, pos = position / 2 pi. The angle in turns is formed and reduced
-// in fp64: its error is about 2^-52 of the whole angle.
+// in fp64: three roundings of 2^-53 of the whole angle (1 / 2 pi and two products), and one of the
+// reduced angle to fp32.
 __device__ __forceinline__ float2 angle(double pos, float freq) {
     const double turns = pos * static_cast<double>(freq);
     float2 cs;
