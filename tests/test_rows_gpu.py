@@ -932,6 +932,64 @@ def test_rows_of_the_most_logits():
             assert (d[1, a:a + (1 << 28)] == d[1, 1]).all()
 
 
+def test_embed_at_the_ends_of_its_range():
+    """The most rows (V = 2^31 - 2, of one element), the widest (D = 2^20) and millions of tokens."""
+    V, pad = (1 << 31) - 2, 4096
+    ids = torch.tensor([V - 1, 0, V, V - 1, -1, 5, V // 2, V - 2], device="cuda")
+    buf = torch.full((pad + V + pad,), 7.0, dtype=BF16, device="cuda")
+    table = buf[pad:pad + V].view(V, 1)
+    dout = torch.arange(1, 9, device="cuda").to(BF16)[:, None]
+    rows.embed_backward(ids, dout, V, 2.0, dtable=table)
+    assert (buf[:pad] == 7).all() and (buf[-pad:] == 7).all()
+    want = [10.0, 4.0, 0.0, 10.0, 0.0, 12.0, 14.0, 16.0]
+    assert rows.embed(ids, table)[:, 0].tolist() == want
+    live = torch.tensor([0, 1, 5, 6, 7], device="cuda")
+    table[ids[live]] = 0
+    assert all((table[a:a + (1 << 28)] == 0).all() for a in range(0, V, 1 << 28))
+    # (one more time, added to what is there)
+    rows.embed_backward(ids, dout, V, 2.0, dtable=table, accumulate=True)
+    assert rows.embed(ids, table)[:, 0].tolist() == want
+    del buf, table
+    D = 1 << 20
+    wide = randn(gen(28), 5, D, dt=BF16)
+    ids = torch.tensor([4, 2, 4, 7], device="cuda")
+    assert same(rows.embed(ids, wide)[:3], wide[[4, 2, 4]])
+    ref, bound = ro.embed_backward(ids, wide[:4], 5, 1.0, BF16)
+    ro.check(rows.embed_backward(ids, wide[:4], 5), ref, bound, "wide")
+    # whole numbers, whose sums are exact in fp32
+    n, V, D = 5_000_001, 1003, 4
+    ids = torch.randint(-3, V + 3, (n,), generator=gen(29)).cuda()
+    dout = torch.randint(-3, 4, (n, D), generator=gen(30)).float().cuda()
+    got = rows.embed_backward(ids, dout, V)
+    ok = (ids >= 0) & (ids < V)
+    ref = torch.zeros(V, D, dtype=torch.float64, device="cuda").index_add_(0, ids[ok], dout[ok].double())
+    assert torch.equal(got.double(), ref)
+
+
+def test_qk_of_many_rows():
+    """2^22 + 5 rows of one head, and 3000 heads of a few rows: every row as in a call of its own."""
+    w, freq = 1 + randn(gen(31), 32, scale=0.2), torch.rand(8, generator=gen(32)).cuda()
+    L = (1 << 22) + 5
+    x, dy = (torch.randn(1, 1, L, 32, generator=torch.Generator("cuda").manual_seed(s), device="cuda").to(BF16)
+             for s in (33, 34))
+    y = rows.qk_norm_rope(x, x, w, w, freq, pos0=3)[0]
+    dx = rows.qk_norm_rope_backward(x, x, dy, dy, w, w, freq, pos0=3)[0]
+    for a, b in ((0, 9), (L // 2, L // 2 + 17), (L - 5, L)):
+        cut = [t[:, :, a:b].contiguous() for t in (x, dy)]
+        assert same(y[:, :, a:b], rows.qk_norm_rope(cut[0], cut[0], w, w, freq, pos0=3 + a)[0])
+        assert same(dx[:, :, a:b], rows.qk_norm_rope_backward(cut[0], cut[0], cut[1], cut[1], w, w, freq, pos0=3 + a)[0])
+    x, dy = randn(gen(35), 2, 3000, 3, 32, dt=F32), randn(gen(36), 2, 3000, 3, 32, dt=F32)
+    y = rows.qk_norm_rope(x, x[:, :1], w, None, freq)[0]
+    g = rows.qk_norm_rope_backward(x, x[:, :1], dy, dy[:, :1], w, None, freq)
+    at = ro.positions_of(3, 0, None)
+    ref, bound = ro.qk_norm_rope(x, w, freq, at, 1e-6, False)
+    ro.check(y, ref, bound, "y")
+    dx, db, dw, wb = ro.qk_norm_rope_backward(x, w, freq, at, dy, 1e-6, False)
+    ro.check(g[0], dx, db, "dx")
+    ro.check(g[2], dw, wb, "dw")
+    assert g[3] is None
+
+
 def test_numbers_of_other_types():
     """numpy's numbers, where a Python number is meant."""
     import numpy as np
